@@ -354,6 +354,200 @@ mpk_status mpk_decode_step_noalloc(const mpk_graph* g, const mpk_weights* w,
                                    int32_t* d_next_tokens, uint32_t* d_status,
                                    void* cuda_stream);
 
+/* ---------------------------------------------------------------------
+ * Serving operators over the paged KV cache: several new tokens a sequence.
+ * (The paper's step takes one token a sequence; these calls are what a
+ * server puts around it: prompts, shared prompts, drafted tokens.)
+ *
+ * Three calls make one step of drafted decoding of a layer and of a batch:
+ *   mpk_kv_append         norm and rotate the new tokens' q and k, append k, v
+ *   mpk_prefix_attention  the new tokens' attention over the cache
+ *   mpk_verify_drafts     accept or refuse the drafts, sample the next token
+ * and mpk_verify_step runs a built graph's whole step with them.
+ *
+ * All of them are asynchronous on `cuda_stream`, allocate nothing and can be
+ * captured into a CUDA graph.  Pointers are device pointers of the current
+ * device unless said otherwise.  Calls that may run at the same time (other
+ * streams, other captured graphs) need workspaces of their own; a workspace
+ * needs no initialisation and holds nothing between calls.
+ * `d_status` (nullable, uint32) keeps the first error a kernel finds (the
+ * kernels only replace MPK_OK; the caller clears it).  After an error the
+ * results of the sequences (for a prefix: of the group) concerned are
+ * unspecified, those of the others are right, and no memory outside the
+ * arguments' is touched. */
+
+/* Heads of one layer and the geometry of its cache (mpk_kv_cache layout).
+ * head_dim is 32, 64 or 128; n_q_heads a multiple of n_kv_heads. */
+typedef struct {
+  int n_q_heads;
+  int n_kv_heads;
+  int head_dim;
+  int page_size;
+  int max_pages_per_seq;
+} mpk_attn_shape;
+
+/* The new tokens of a batch, as the rows of token-major tensors.  Sequence b
+ * owns rows [q_start[b], q_start[b + 1]), none if the two are equal; with a
+ * null q_start it owns [b * tokens_per_seq, (b + 1) * tokens_per_seq).  Row i
+ * of sequence b (from 0) stands at position seq_lens[b] + i.  Rows outside
+ * every sequence (padding behind the last) are neither read nor written. */
+typedef struct {
+  int batch;
+  int n_tokens;             /* rows of the tensors                          */
+  const int32_t* q_start;   /* nullable, int32 [batch + 1], ascending       */
+  int tokens_per_seq;
+} mpk_token_batch;
+
+/* Rotary positions.  The table is fp32 [n_pos][rotary_dim / 2][2] (cos, sin),
+ * row p for position p (mpk_rope_table writes one; mpk_decode_step's own is
+ * the one of scaling MPK_ROPE_PLAIN).  The first rotary_dim values of a head
+ * are rotated (a multiple of 16, at most head_dim; 0: none), in pairs
+ * (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved != 0. */
+typedef struct {
+  const float* table;
+  int n_pos;
+  int rotary_dim;
+  int interleaved;
+} mpk_rope;
+
+/* Scaling of the frequencies f_i = theta^(-2i / rotary_dim) for contexts
+ * longer than the trained old_ctx. */
+enum {
+  MPK_ROPE_PLAIN = 0,   /* f_i                                              */
+  MPK_ROPE_LINEAR = 1,  /* f_i / factor                                     */
+  MPK_ROPE_BANDS = 2,   /* a mixture of f_i / factor and f_i by the turns
+                           t_i = old_ctx f_i / 2 pi a pair makes: all of the
+                           first for t_i <= low, of the second for
+                           t_i >= high, linear in t_i between               */
+  MPK_ROPE_RAMP = 3     /* the same mixture, linear in i between (the whole
+                           numbers around) the indices of high and low turns */
+};
+typedef struct {
+  int rotary_dim;
+  double theta;
+  int scaling;            /* MPK_ROPE_*                                     */
+  double factor;          /* > 0; unused by MPK_ROPE_PLAIN                  */
+  double low, high;       /* 0 < low < high  (BANDS, RAMP)                  */
+  double old_ctx;         /* > 0             (BANDS, RAMP)                  */
+  double attn_factor;     /* multiplies every cos and sin; 0 means 1        */
+} mpk_rope_scaling;
+
+/* Write rows [first_pos, first_pos + n_pos) of a rotation table to d_table
+ * (fp32 [n_pos][rotary_dim / 2][2]).  Angles are formed in 64 bits. */
+mpk_status mpk_rope_table(const mpk_rope_scaling* s, int64_t first_pos,
+                          int n_pos, float* d_table, void* cuda_stream);
+
+/* New tokens into layer `layer` of the cache.  d_q, d_k, d_v: bf16 rows of
+ * heads, [n_tokens][heads * head_dim] with row strides in elements (the
+ * parts of a fused projection's rows, or separate tensors).  q and k get a
+ * per-head RMSNorm with gains d_q_norm / d_k_norm (bf16 [head_dim], nullable:
+ * none; rounded to bf16) and the rotation of *rope (nullable: none), with the
+ * arithmetic and roundings of mpk_decode_step; v goes in as it is.  Rotated q
+ * goes to d_q_out (its own row stride; it may be d_q itself; null: q is not
+ * touched).  seq_lens is read, not advanced.  Pointers 16-byte aligned,
+ * strides multiples of 8.
+ * Errors in d_status: MPK_ERR_KV_PAGE for a position without a page,
+ * MPK_ERR_INVALID_ARG for one past the table; such a token is skipped. */
+mpk_status mpk_kv_append(const mpk_attn_shape* shape,
+                         const mpk_token_batch* tok, const mpk_kv_cache* kv,
+                         int layer, const void* d_q, int64_t q_stride,
+                         const void* d_k, int64_t k_stride, const void* d_v,
+                         int64_t v_stride, const void* d_q_norm,
+                         const void* d_k_norm, float eps,
+                         const mpk_rope* rope, void* d_q_out,
+                         int64_t q_out_stride, uint32_t* d_status,
+                         void* cuda_stream);
+
+/* Groups of consecutive sequences that share their first tokens: group g is
+ * sequences [group_start[g], group_start[g + 1]), ascending from 0 to the
+ * batch, and positions [0, prefix_len[g]) of all of them hold the same keys
+ * and values; these are read through the page table row of the group's
+ * FIRST sequence, once for the whole group (the other rows may map the same
+ * pages or anything else there).  Every sequence of the group with new tokens
+ * must have seq_lens >= prefix_len (else MPK_ERR_INVALID_ARG in d_status).
+ * A prefix_len of 0 is no prefix. */
+typedef struct {
+  int n_groups;                /* 1 .. batch                                */
+  const int32_t* group_start;  /* device int32 [n_groups + 1]               */
+  const int32_t* prefix_len;   /* device int32 [n_groups]                   */
+} mpk_prefix_groups;
+
+/* Bytes of workspace that mpk_prefix_attention needs (0 for arguments that
+ * it refuses).  n_groups: 0 without groups. */
+size_t mpk_prefix_attention_workspace(const mpk_attn_shape* shape,
+                                      const mpk_token_batch* tok,
+                                      int n_groups);
+
+/* Attention of the new tokens of layer `layer`, whose keys and values are in
+ * the cache already (mpk_kv_append): row at position t sees keys 0..t.
+ * d_q bf16 [n_tokens][n_q_heads * head_dim] (row stride in elements), d_out
+ * the same (its own stride; not d_q), d_lse (nullable) fp32
+ * [n_tokens][n_q_heads]: log of the row's sum of exponentials.  Query head j
+ * reads KV head j / (n_q_heads / n_kv_heads).  scale multiplies the scores;
+ * 0 selects 1/sqrt(head_dim).  groups may be null.  A row that sees no key
+ * gives zeros and -inf.  Values that are not finite at keys a row does not
+ * see do not reach it.  Pointers 16-byte aligned (d_lse 4), strides
+ * multiples of 8; d_workspace 256-byte aligned.  At most 2^20 sequences. */
+mpk_status mpk_prefix_attention(const mpk_attn_shape* shape,
+                                const mpk_token_batch* tok,
+                                const mpk_prefix_groups* groups,
+                                const mpk_kv_cache* kv, int layer,
+                                const void* d_q, int64_t q_stride, float scale,
+                                void* d_out, int64_t out_stride, float* d_lse,
+                                void* d_workspace, size_t workspace_bytes,
+                                uint32_t* d_status, void* cuda_stream);
+
+/* Inputs and outputs of mpk_verify_drafts.  Row i of sequence b holds token
+ * tokens[row] (i = 0: the last token accepted before, i >= 1: draft i), and
+ * logits[row] are the model's after that token, so row i judges draft i + 1
+ * and a sequence of n rows has n - 1 drafts (at most 127).  A draft outside
+ * [0, vocab) ends its sequence's drafts (as if all before it were all).
+ * p = softmax(logits / T).  draft row i says what draft i + 1 was drawn from:
+ * probabilities, or (draft_is_logits) logits taken at the same T; null: the
+ * drafts were chosen outright, q = 1.  Draft i + 1 is accepted when
+ * uniform[row i] * q < p; at the first refusal the next token is
+ * argmax_v max(p_v - q_v, 0) / noise[b][v] (p alone where that is nowhere
+ * positive; without `draft`, p without the refused token), and with all
+ * accepted argmax_v p_v / noise[b][v] of the last row; ties take the lowest
+ * index.  With uniform in [0, 1) and noise ~ Exp(1), the emitted tokens are
+ * distributed as samples of p.  T <= 0 is greedy: a draft is accepted when it
+ * is the row's argmax, the next token is the argmax.  NaN logits count as
+ * -inf, several +inf share the row; a row of nothing but -inf accepts nothing
+ * and gives token -1. */
+typedef struct {
+  int vocab;
+  int max_out;               /* columns of out_tokens, >= rows of a sequence */
+  const int32_t* tokens;     /* [n_tokens]                                  */
+  const float* logits;       /* [n_tokens], row stride logits_stride        */
+  int64_t logits_stride;     /* elements                                    */
+  const float* draft;        /* nullable [n_tokens], row stride draft_stride */
+  int64_t draft_stride;
+  int draft_is_logits;
+  const float* temperature;  /* nullable [batch]; null: 1                   */
+  const float* uniform;      /* [n_tokens]                                  */
+  const float* noise;        /* [batch], row stride noise_stride            */
+  int64_t noise_stride;
+  int32_t* n_accepted;       /* out [batch]                                 */
+  int32_t* out_tokens;       /* out [batch][max_out]: the accepted drafts,
+                                the next token, then -1                     */
+  float* logprobs;           /* out, nullable [batch][max_out]: log p of each
+                                (0 when greedy and for -1)                  */
+  int32_t* next_tokens;      /* out, nullable [batch]: the next token       */
+  const int32_t* seq_lens;   /* nullable [batch]                            */
+  int32_t* seq_lens_out;     /* out, nullable [batch], may be seq_lens:
+                                seq_lens + n_accepted + 1 (unchanged for a
+                                sequence without rows)                      */
+} mpk_verify_args;
+
+size_t mpk_verify_drafts_workspace(const mpk_token_batch* tok, int vocab);
+
+/* One launch pair over the batch; see mpk_verify_args.  Float pointers need
+ * 4-byte alignment only; d_workspace 256. */
+mpk_status mpk_verify_drafts(const mpk_token_batch* tok,
+                             const mpk_verify_args* args, void* d_workspace,
+                             size_t workspace_bytes, uint32_t* d_status,
+                             void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,6 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libmpk.so")
 BUILD_DIR = os.path.join(PKG, "_build")
+SERVE = ["append", "attend", "verify"]   # serving operators' kernels
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -49,6 +50,15 @@ def build(verbose: bool = False) -> str:
         [nvcc] + ARCH + ["-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-c",
                          os.path.join(CSRC, "noalloc.cu"), "-o",
                          os.path.join(BUILD_DIR, "noalloc.o")] + inc,
+    ] + [
+        [nvcc] + ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler",
+                         "-fPIC", "-c", os.path.join(CSRC, name + ".cu"),
+                         "-o", os.path.join(BUILD_DIR, name + ".o")] + inc
+        for name in SERVE
+    ] + [
+        ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-c",
+         os.path.join(CSRC, "serve_api.cpp"), "-o",
+         os.path.join(BUILD_DIR, "serve_api.o")] + inc,
         ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-c",
          os.path.join(CSRC, "capi.cpp"), "-o",
          os.path.join(BUILD_DIR, "capi.o")] + inc,
@@ -70,6 +80,8 @@ def build(verbose: bool = False) -> str:
     _run([nvcc] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp,
                           os.path.join(BUILD_DIR, "kernels.o"),
                           os.path.join(BUILD_DIR, "noalloc.o"),
+                          os.path.join(BUILD_DIR, "serve_api.o"),
+                          *[os.path.join(BUILD_DIR, n + ".o") for n in SERVE],
                           os.path.join(BUILD_DIR, "capi.o"),
                           os.path.join(BUILD_DIR, "tgraph_builder.o"),
                           os.path.join(BUILD_DIR, "layout.o"),

@@ -1,0 +1,186 @@
+// How the attention kernels share out their work, worked out by every CTA
+// from the device arrays (sequence lengths are not known to the host).
+//
+// Entities are the groups (a prefix and the rows of all its sequences) and
+// then the sequences (own keys and own rows).  An entity's rows are cut into
+// tiles of M, its keys into blocks of BN; a unit is one (row tile, KV head).
+// All blocks of all units form one line, of which every CTA takes an equal
+// stretch: the load is even whatever the lengths are, and a long key axis is
+// split when there are few rows.  A stretch of one unit's blocks is a
+// segment; its partial result goes to slot (unit + CTA), which is unique
+// because along the line either number grows from one segment to the next.
+// The unit's slots are consecutive, so the merge needs only the first and
+// the count.
+#pragma once
+
+#include "serve_dev.cuh"
+
+namespace mpk {
+
+struct Ent {
+  int tok0, rows;   // first token row, rows = tokens * query heads per KV head
+  int k0, k1;       // keys
+  int seq;          // whose page table row
+};
+
+__device__ __forceinline__ int att_ctx(const PagedArgs& p) {
+  const int64_t c = (int64_t)p.max_pages * p.page_size;
+  return c > 0x7fffffff ? 0x7fffffff : (int)c;
+}
+__device__ __forceinline__ int att_group(const AttendArgs& a, int b) {
+  if (a.n_groups <= 1) return 0;
+  int lo = 0, hi = a.n_groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.group_start + mid) <= b) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+__device__ __forceinline__ int att_prefix(const AttendArgs& a, int g) {
+  if (a.n_groups == 0) return 0;
+  return min(max(__ldg(a.prefix_len + g), 0), att_ctx(a.p));
+}
+__device__ __forceinline__ Ent att_group_ent(const AttendArgs& a, int g) {
+  const PagedArgs& p = a.p;
+  Ent e;
+  const int b0 = min(max(__ldg(a.group_start + g), 0), p.batch);
+  const int b1 = min(max(__ldg(a.group_start + g + 1), b0), p.batch);
+  e.tok0 = sv_row(p.q_start, p.tokens_per_seq, p.n_tokens, b0);
+  const int t1 = sv_row(p.q_start, p.tokens_per_seq, p.n_tokens, b1);
+  e.rows = max(t1 - e.tok0, 0) * (p.Hq / p.Hkv);
+  e.k0 = 0;
+  e.k1 = att_prefix(a, g);
+  e.seq = min(b0, p.batch - 1);
+  return e;
+}
+__device__ __forceinline__ Ent att_seq_ent(const AttendArgs& a, int b) {
+  const PagedArgs& p = a.p;
+  Ent e;
+  e.tok0 = sv_row(p.q_start, p.tokens_per_seq, p.n_tokens, b);
+  const int n =
+      max(sv_row(p.q_start, p.tokens_per_seq, p.n_tokens, b + 1) - e.tok0, 0);
+  e.rows = n * (p.Hq / p.Hkv);
+  const int len = __ldg(p.seq_lens + b);
+  e.k0 = att_prefix(a, att_group(a, b));
+  const int64_t end = (int64_t)len + n;
+  const int ctx = att_ctx(p);
+  e.k1 = end > ctx ? ctx : (int)end;
+  e.seq = b;
+  if (n > 0 && (end > ctx || len < 0)) sv_latch(p.status, MPK_ERR_KV_PAGE);
+  // the prefix is read for every row of the group, so each sequence has to
+  // hold all of it
+  if (n > 0 && len < e.k0) {
+    sv_latch(p.status, MPK_ERR_INVALID_ARG);
+    e.k1 = e.k0;
+  }
+  if (e.k1 < e.k0) e.k1 = e.k0;
+  return e;
+}
+
+// Where a CTA starts on the line.
+struct PlanStart {
+  int64_t x0, x1;      // this CTA's stretch
+  int64_t total;       // blocks of all units
+  int64_t off;         // x0 within entity e
+  int64_t unit0;       // units before entity e
+  int e;
+  int n;               // CTAs that take part
+};
+
+// Finds the CTA's stretch with one scan over the entities (NT threads).
+// Both passes of a batch of more than NT entities read the arrays again.
+// `ent(e)` gives entity e.
+template <int NT, int M, int BN, typename F>
+__device__ __forceinline__ PlanStart plan_start(int n_ent, int Hkv, F ent,
+                                                int cta, int n_cta) {
+  __shared__ int64_t sh_cost[NT / 32], sh_unit[NT / 32];
+  __shared__ int64_t sh_off, sh_base;
+  __shared__ int sh_e;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto blocks = [&](int i, int64_t& cost, int64_t& unit) {
+    cost = unit = 0;
+    if (i < n_ent) {
+      const Ent e = ent(i);
+      const int64_t nb = (e.k1 - e.k0 + BN - 1) / BN;
+      const int64_t nt = (e.rows + M - 1) / M;
+      cost = nb * nt * Hkv;
+      unit = nb > 0 ? nt * Hkv : 0;
+    }
+  };
+  int64_t cost, unit, total = 0;
+  blocks(tid, cost, unit);
+  {
+    int64_t mine = cost, c2, u2;
+    for (int i = tid + NT; i < n_ent; i += NT) {
+      blocks(i, c2, u2);
+      mine += c2;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) sh_cost[warp] = mine;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) total += sh_cost[w];
+  }
+  PlanStart st;
+  st.total = total;
+  // every CTA that takes part has a block, so a unit's segments belong to
+  // consecutive CTAs
+  st.n = total < n_cta ? (int)total : n_cta;
+  st.x0 = cta < st.n ? total * cta / st.n : total;
+  st.x1 = cta < st.n ? total * (cta + 1) / st.n : total;
+  if (tid == 0) sh_e = n_ent;
+  int64_t run_c = 0, run_u = 0;
+  for (int i0 = 0; i0 < n_ent; i0 += NT) {
+    if (i0 > 0) blocks(i0 + tid, cost, unit);
+    int64_t ic = cost, iu = unit;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t vc = __shfl_up_sync(0xffffffffu, ic, o);
+      const int64_t vu = __shfl_up_sync(0xffffffffu, iu, o);
+      if (lane >= o) {
+        ic += vc;
+        iu += vu;
+      }
+    }
+    __syncthreads();
+    if (lane == 31) {
+      sh_cost[warp] = ic;
+      sh_unit[warp] = iu;
+    }
+    __syncthreads();
+    int64_t bc = run_c, bu = run_u;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+      if (w < warp) {
+        bc += sh_cost[w];
+        bu += sh_unit[w];
+      }
+      run_c += sh_cost[w];
+      run_u += sh_unit[w];
+    }
+    bc += ic - cost;
+    bu += iu - unit;
+    if (cost > 0 && st.x0 >= bc && st.x0 < bc + cost) {
+      sh_e = i0 + tid;
+      sh_off = st.x0 - bc;
+      sh_base = bu;
+    }
+    if (run_c > st.x0) break;
+  }
+  __syncthreads();
+  st.e = sh_e;
+  st.off = sh_off;
+  st.unit0 = sh_base;
+  return st;
+}
+
+// CTA that owns position x of the line.
+__device__ __forceinline__ int plan_owner(int64_t x, int64_t total,
+                                          int n_cta) {
+  return (int)(((x + 1) * n_cta - 1) / total);
+}
+
+}  // namespace mpk

@@ -98,6 +98,55 @@ class GraphExport(ctypes.Structure):
         ("n_sched_sms", ctypes.c_int), ("sched_warps_per_sm", ctypes.c_int)]
 
 
+class AttnShape(ctypes.Structure):
+    _fields_ = [("n_q_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("max_pages_per_seq", ctypes.c_int)]
+
+
+class TokenBatch(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("n_tokens", ctypes.c_int),
+                ("q_start", ctypes.c_void_p),
+                ("tokens_per_seq", ctypes.c_int)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_pos", ctypes.c_int),
+                ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int)]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("theta", ctypes.c_double),
+                ("scaling", ctypes.c_int), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("old_ctx", ctypes.c_double),
+                ("attn_factor", ctypes.c_double)]
+
+
+class PrefixGroups(ctypes.Structure):
+    _fields_ = [("n_groups", ctypes.c_int), ("group_start", ctypes.c_void_p),
+                ("prefix_len", ctypes.c_void_p)]
+
+
+class VerifyArgs(ctypes.Structure):
+    _fields_ = [("vocab", ctypes.c_int), ("max_out", ctypes.c_int),
+                ("tokens", ctypes.c_void_p), ("logits", ctypes.c_void_p),
+                ("logits_stride", ctypes.c_int64),
+                ("draft", ctypes.c_void_p), ("draft_stride", ctypes.c_int64),
+                ("draft_is_logits", ctypes.c_int),
+                ("temperature", ctypes.c_void_p),
+                ("uniform", ctypes.c_void_p), ("noise", ctypes.c_void_p),
+                ("noise_stride", ctypes.c_int64),
+                ("n_accepted", ctypes.c_void_p),
+                ("out_tokens", ctypes.c_void_p),
+                ("logprobs", ctypes.c_void_p),
+                ("next_tokens", ctypes.c_void_p),
+                ("seq_lens", ctypes.c_void_p),
+                ("seq_lens_out", ctypes.c_void_p)]
+
+
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BANDS, ROPE_RAMP = 0, 1, 2, 3
+
 _lib = None
 
 
@@ -112,6 +161,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "`python -m task_graph_runtime_gb300.build` (no fallback exists)")
     lib = ctypes.CDLL(path)
     vp, i, st = ctypes.c_void_p, ctypes.c_int, ctypes.c_int
+    i64 = ctypes.c_int64
     sig = {
         "mpk_build_tgraph": ([ctypes.POINTER(ModelShape),
                               ctypes.POINTER(TileSizes), i,
@@ -137,6 +187,26 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "mpk_decode_step_noalloc": ([vp, ctypes.POINTER(_Weights), vp,
                                      ctypes.POINTER(_KVCache), vp, vp, vp,
                                      vp], st),
+        "mpk_rope_table": ([ctypes.POINTER(RopeScaling), i64, i, vp, vp], st),
+        "mpk_kv_append": ([ctypes.POINTER(AttnShape),
+                           ctypes.POINTER(TokenBatch),
+                           ctypes.POINTER(_KVCache), i, vp, i64, vp, i64, vp,
+                           i64, vp, vp, ctypes.c_float,
+                           ctypes.POINTER(_Rope), vp, i64, vp, vp], st),
+        "mpk_prefix_attention_workspace": ([ctypes.POINTER(AttnShape),
+                                            ctypes.POINTER(TokenBatch), i],
+                                           ctypes.c_size_t),
+        "mpk_prefix_attention": ([ctypes.POINTER(AttnShape),
+                                  ctypes.POINTER(TokenBatch),
+                                  ctypes.POINTER(PrefixGroups),
+                                  ctypes.POINTER(_KVCache), i, vp, i64,
+                                  ctypes.c_float, vp, i64, vp, vp,
+                                  ctypes.c_size_t, vp, vp], st),
+        "mpk_verify_drafts_workspace": ([ctypes.POINTER(TokenBatch), i],
+                                        ctypes.c_size_t),
+        "mpk_verify_drafts": ([ctypes.POINTER(TokenBatch),
+                               ctypes.POINTER(VerifyArgs), vp,
+                               ctypes.c_size_t, vp, vp], st),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -390,3 +460,290 @@ def mpk_decode_step_noalloc(graph: "Graph", weights: Weights, tokens, kv,
         status.data_ptr() if status is not None else None, s),
         "mpk_decode_step_noalloc")
     return layers          # keep the host pointer array alive until here
+
+
+# ------------------------------------------------------- serving operators
+def _stream_of(stream, device):
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _refuse(where: str, what: str):
+    raise MpkError(MPK_ERR_INVALID_ARG, f"{where}: {what}")
+
+
+class _OnDevice:
+    """Calls go to the tensors' own device, whichever one is current."""
+
+    def _call(self, fn, *args):
+        import torch
+        if torch.cuda.current_device() == self.device.index:
+            return fn(*args)
+        with torch.cuda.device(self.device):
+            return fn(*args)
+
+    def _vec(self, t, n, dtype, where, name):
+        """Device pointer of a contiguous vector of at least n values."""
+        if t is None:
+            return None
+        if (t.dtype is not dtype or t.device != self.device or
+                t.numel() < n or not t.is_contiguous()):
+            _refuse(where, f"{name} must be a contiguous {dtype} tensor of "
+                           f"{n} values on {self.device}")
+        return t.data_ptr()
+
+
+def _cuda_device(t, where):
+    if t.device.type != "cuda":
+        _refuse(where, f"tensors must be on a CUDA device, not {t.device}")
+    return t.device
+
+
+def mpk_rope_table(rotary_dim: int, n_pos: int, theta: float,
+                   first_pos: int = 0, scaling: int = ROPE_PLAIN,
+                   factor: float = 1.0, low: float = 1.0, high: float = 4.0,
+                   old_ctx: float = 8192.0, attn_factor: float = 1.0,
+                   device="cuda", stream=None):
+    """fp32 [n_pos, rotary_dim // 2, 2] table of (cos, sin) for positions
+    first_pos, first_pos + 1, ...; see include/mpk.h for the scalings."""
+    import torch
+    out = torch.empty(max(n_pos, 0), max(rotary_dim, 0) // 2, 2,
+                      dtype=torch.float32, device=device)
+    dev = _cuda_device(out, "mpk_rope_table")
+    s = RopeScaling(rotary_dim, theta, scaling, factor, low, high, old_ctx,
+                    attn_factor)
+    with torch.cuda.device(dev):
+        _check(load_library().mpk_rope_table(
+            ctypes.byref(s), first_pos, n_pos, out.data_ptr() or None,
+            _stream_of(stream, dev)), "mpk_rope_table")
+    return out
+
+
+class Rope:
+    """A rotation table (``mpk_rope_table``) and how heads use it."""
+
+    def __init__(self, table, rotary_dim: int, interleaved: bool = False):
+        import torch
+        dev = _cuda_device(table, "Rope")
+        if (table.dtype is not torch.float32 or not table.is_contiguous() or
+                table.dim() != 3 or tuple(table.shape[1:]) !=
+                (rotary_dim // 2, 2)):
+            _refuse("Rope", "table must be contiguous float32 "
+                            "[n_pos, rotary_dim // 2, 2]")
+        self.table = table
+        self.device = dev
+        self.c = _Rope(table.data_ptr(), int(table.shape[0]), rotary_dim,
+                       int(bool(interleaved)))
+        self.ref = ctypes.byref(self.c)
+
+
+class PagedBatch(_OnDevice):
+    """New tokens of a batch over a paged cache: what a server keeps while
+    the batch's composition stays.  ``q_start`` (int32 [batch + 1]) gives each
+    sequence's rows; without it every sequence has n_tokens // batch.
+    ``group_start`` / ``prefix_len`` name the sequences that share a prefix
+    (include/mpk.h: mpk_prefix_groups).  The arrays are read on the device by
+    every call, so their contents may change between calls.  ``status``
+    (int32 [1], optional) keeps the first error the kernels find.  The
+    workspace is this object's own, allocated by the first ``attend``: calls
+    of one object must not overlap on the GPU."""
+
+    def __init__(self, kv: KVCache, n_q_heads: int, n_tokens: int,
+                 q_start=None, group_start=None, prefix_len=None,
+                 status=None):
+        import torch
+        w = "PagedBatch"
+        k, v = kv.k_pool, kv.v_pool
+        self.device = _cuda_device(k, w)
+        if (k.dim() != 5 or k.dtype is not torch.bfloat16 or
+                v.dtype is not torch.bfloat16 or v.shape != k.shape or
+                not k.is_contiguous() or not v.is_contiguous() or
+                v.device != self.device):
+            _refuse(w, "k_pool and v_pool must be contiguous bfloat16 "
+                       "[layers, pages, kv_heads, page_size, head_dim]")
+        if kv.page_table.dim() != 2:
+            _refuse(w, "page_table must be [batch, max_pages_per_seq]")
+        batch, cols = (int(x) for x in kv.page_table.shape)
+        self._vec(kv.page_table, 0, torch.int32, w, "page_table")
+        self._vec(kv.seq_lens, batch, torch.int32, w, "seq_lens")
+        qs = self._vec(q_start, batch + 1, torch.int32, w, "q_start")
+        if batch < 1 or n_tokens < 0 or (qs is None and n_tokens % batch):
+            _refuse(w, "n_tokens must be a multiple of the batch without "
+                       "q_start")
+        st = self._vec(status, 1, torch.int32, w, "status")
+        self.kv, self.n_layers = kv, int(k.shape[0])
+        self.n_tokens, self.batch = n_tokens, batch
+        self.q_width = n_q_heads * int(k.shape[4])
+        self.kv_width = int(k.shape[2]) * int(k.shape[4])
+        self.n_q_heads, self.head_dim = n_q_heads, int(k.shape[4])
+        self._shape = AttnShape(n_q_heads, int(k.shape[2]), int(k.shape[4]),
+                                int(k.shape[3]), cols)
+        self._tok = TokenBatch(batch, n_tokens, qs, n_tokens // batch)
+        self._kv = kv.c_struct()
+        self._groups = None
+        if (group_start is None) != (prefix_len is None):
+            _refuse(w, "group_start and prefix_len come together")
+        if prefix_len is not None:
+            n = int(prefix_len.numel())
+            self._groups = PrefixGroups(
+                n, self._vec(group_start, n + 1, torch.int32, w,
+                             "group_start"),
+                self._vec(prefix_len, n, torch.int32, w, "prefix_len"))
+            if n < 1 or n > batch:
+                _refuse(w, "1 to batch groups")
+        self._keep = (q_start, group_start, prefix_len, status)
+        self._st = st
+        self._refs = (ctypes.byref(self._shape), ctypes.byref(self._tok),
+                      ctypes.byref(self._kv),
+                      ctypes.byref(self._groups) if self._groups else None)
+        self._ws = None
+        self._lib = load_library()
+
+    def _rows(self, t, width, where, name):
+        """Pointer and row stride of [n_tokens, width] (or [n_tokens, heads,
+        head_dim]) bf16 rows whose values lie side by side."""
+        import torch
+        sh, n = t.shape, self.n_tokens
+        ok = t.dtype is torch.bfloat16 and t.device == self.device
+        if ok and len(sh) == 2:
+            ok = sh[0] >= n and sh[1] == width and t.stride(1) == 1
+        elif ok and len(sh) == 3:
+            ok = (sh[0] >= n and sh[2] == self.head_dim and
+                  sh[1] * sh[2] == width and t.stride(2) == 1 and
+                  (sh[1] == 1 or t.stride(1) == sh[2]))
+        else:
+            ok = False
+        if not ok:
+            _refuse(where, f"{name} must be bfloat16 [{n}, {width}] on "
+                           f"{self.device} with contiguous rows")
+        return t.data_ptr(), (t.stride(0) if n > 1 else width)
+
+    def _layer(self, layer, where):
+        if not 0 <= layer < self.n_layers:
+            _refuse(where, f"layer {layer} of {self.n_layers}")
+
+    def append(self, layer: int, q, k, v, rope: Optional[Rope] = None,
+               q_out=None, q_norm=None, k_norm=None, eps: float = 1e-6,
+               stream=None):
+        """mpk_kv_append: norm and rotate q and k, append k and v.  q may be
+        None when q_out is."""
+        import torch
+        w = "PagedBatch.append"
+        self._layer(layer, w)
+        if q_out is not None and q is None:
+            _refuse(w, "q_out without q")
+        qp = self._rows(q, self.q_width, w, "q") if q_out is not None \
+            else (None, 0)
+        kp = self._rows(k, self.kv_width, w, "k")
+        vp = self._rows(v, self.kv_width, w, "v")
+        op = self._rows(q_out, self.q_width, w, "q_out") \
+            if q_out is not None else (None, 0)
+        if rope is not None and rope.device != self.device:
+            _refuse(w, "rope is on another device")
+        d, bf = self.head_dim, torch.bfloat16
+        _check(self._call(
+            self._lib.mpk_kv_append, *self._refs[:3], layer, *qp, *kp, *vp,
+            self._vec(q_norm, d, bf, w, "q_norm"),
+            self._vec(k_norm, d, bf, w, "k_norm"), eps,
+            rope.ref if rope is not None else None, *op, self._st,
+            _stream_of(stream, self.device)), "mpk_kv_append")
+
+    def attend(self, layer: int, q, out, lse=None, scale: float = 0.0,
+               stream=None):
+        """mpk_prefix_attention of the new tokens over the cache."""
+        import torch
+        w = "PagedBatch.attend"
+        self._layer(layer, w)
+        qp = self._rows(q, self.q_width, w, "q")
+        op = self._rows(out, self.q_width, w, "out")
+        lp = self._vec(lse, self.n_tokens * self.n_q_heads, torch.float32, w,
+                       "lse")
+        if self._ws is None:
+            n = self._lib.mpk_prefix_attention_workspace(
+                self._refs[0], self._refs[1],
+                self._groups.n_groups if self._groups else 0)
+            self._ws = torch.empty(max(n, 1), dtype=torch.uint8,
+                                   device=self.device)
+        _check(self._call(
+            self._lib.mpk_prefix_attention, self._refs[0], self._refs[1],
+            self._refs[3], self._refs[2], layer, *qp, scale, *op, lp,
+            self._ws.data_ptr(), self._ws.numel(), self._st,
+            _stream_of(stream, self.device)), "mpk_prefix_attention")
+
+
+class DraftVerifier(_OnDevice):
+    """mpk_verify_drafts with a workspace of its own (calls of one object must
+    not overlap on the GPU).  ``n_tokens`` rows of ``batch`` sequences, at most
+    ``max_out`` rows each."""
+
+    def __init__(self, batch: int, n_tokens: int, vocab: int, max_out: int,
+                 device="cuda", status=None):
+        import torch
+        w = "DraftVerifier"
+        probe = torch.empty(0, dtype=torch.uint8, device=device)
+        self.device = _cuda_device(probe, w)
+        self.batch, self.n_tokens = batch, n_tokens
+        self.vocab, self.max_out = vocab, max_out
+        self._lib = load_library()
+        self._tok = TokenBatch(batch, n_tokens, None, 0)
+        n = self._lib.mpk_verify_drafts_workspace(ctypes.byref(self._tok),
+                                                  vocab)
+        if n == 0 or not 1 <= max_out <= 128:
+            raise MpkError(MPK_ERR_UNSUPPORTED if max_out > 128 else
+                           MPK_ERR_INVALID_ARG, w)
+        self._ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        self._status = status
+        self._st = self._vec(status, 1, torch.int32, w, "status")
+        self._args = VerifyArgs()
+
+    def _matrix(self, t, rows, where, name):
+        import torch
+        if t is None:
+            return None, 0
+        if (t.dtype is not torch.float32 or t.device != self.device or
+                t.dim() != 2 or t.shape[0] < rows or
+                t.shape[1] != self.vocab or
+                (self.vocab > 1 and t.stride(1) != 1)):
+            _refuse(where, f"{name} must be float32 [{rows}, {self.vocab}] on "
+                           f"{self.device} with contiguous rows")
+        return t.data_ptr(), (t.stride(0) if rows > 1 else self.vocab)
+
+    def verify(self, tokens, logits, uniform, noise, n_accepted, out_tokens,
+               q_start=None, draft=None, draft_is_logits: bool = False,
+               temperature=None, logprobs=None, next_tokens=None,
+               seq_lens=None, seq_lens_out=None, stream=None):
+        """Accept or refuse the drafts and sample the next tokens; arguments
+        and outputs as in include/mpk.h (mpk_verify_args)."""
+        import torch
+        w = "DraftVerifier.verify"
+        B, n, i32, f32 = self.batch, self.n_tokens, torch.int32, torch.float32
+        self._tok.q_start = self._vec(q_start, B + 1, i32, w, "q_start")
+        if q_start is None and n % B:
+            _refuse(w, "n_tokens must be a multiple of the batch without "
+                       "q_start")
+        self._tok.tokens_per_seq = n // B
+        lg = self._matrix(logits, n, w, "logits")
+        dr = self._matrix(draft, n, w, "draft")
+        no = self._matrix(noise, B, w, "noise")
+        bo = B * self.max_out
+        a = self._args
+        a.vocab, a.max_out = self.vocab, self.max_out
+        a.tokens = self._vec(tokens, n, i32, w, "tokens")
+        a.logits, a.logits_stride = lg
+        a.draft, a.draft_stride = dr
+        a.draft_is_logits = int(bool(draft_is_logits))
+        a.temperature = self._vec(temperature, B, f32, w, "temperature")
+        a.uniform = self._vec(uniform, n, f32, w, "uniform")
+        a.noise, a.noise_stride = no
+        a.n_accepted = self._vec(n_accepted, B, i32, w, "n_accepted")
+        a.out_tokens = self._vec(out_tokens, bo, i32, w, "out_tokens")
+        a.logprobs = self._vec(logprobs, bo, f32, w, "logprobs")
+        a.next_tokens = self._vec(next_tokens, B, i32, w, "next_tokens")
+        a.seq_lens = self._vec(seq_lens, B, i32, w, "seq_lens")
+        a.seq_lens_out = self._vec(seq_lens_out, B, i32, w, "seq_lens_out")
+        _check(self._call(
+            self._lib.mpk_verify_drafts, ctypes.byref(self._tok),
+            ctypes.byref(a), self._ws.data_ptr(), self._ws.numel(), self._st,
+            _stream_of(stream, self.device)), "mpk_verify_drafts")
