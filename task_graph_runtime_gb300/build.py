@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libmpk.so")
 BUILD_DIR = os.path.join(PKG, "_build")
-SERVE = ["append", "attend", "verify"]   # serving operators' kernels
+# the serving operators' kernels
+SERVE = ["append", "attend", "attend_tc", "verify"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -100,6 +100,7 @@ struct Body {
   static constexpr int RSTEP = kNT / CH;
 
   const AttendArgs& a;
+  const AttnSet& set;
   uint8_t* smem;
   float (*s_ml)[2];   // [WN][M] of each warp
   uint32_t* s_bad;    // [2] keys of a block whose V is not finite
@@ -287,8 +288,8 @@ struct Body {
     }
     cp_wait<0>();
     __syncthreads();      // the ring is free
-    float* part = a.own.part + slot * M * D;
-    float2* ml = a.own.ml + slot * M;
+    float* part = set.part + slot * M * D;
+    float2* ml = set.ml + slot * M;
     if (WN == 1) {
       // rows of a warp are complete
 #pragma unroll
@@ -416,26 +417,31 @@ struct Body {
   }
 };
 
+// Entities of a launch: groups and sequences, or only one of the two.
+enum { ENT_BOTH, ENT_GROUPS, ENT_SEQS };
+
 template <int D, int WM>
 __global__ void __launch_bounds__(kNT)
-    attend_kernel(const __grid_constant__ AttendArgs a) {
+    attend_kernel(const __grid_constant__ AttendArgs a, int what) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int M = Cfg<D, WM>::M, WN = Cfg<D, WM>::WN;
   __shared__ float s_ml[WN * M][2];
   __shared__ uint32_t s_bad[2];
-  // After the tensor-memory kernel (which has waited for everything before
+  // Behind a launch for the prefixes (which has waited for everything before
   // it) nothing here depends on its results: start at once, and wait for it
   // at the end so that the merge, which waits for this kernel, has both.
-  if (!a.tc) sv_grid_wait();
+  if (what != ENT_SEQS || a.split == ATT_ONE) sv_grid_wait();
   sv_grid_launch();
-  const int G = a.tc ? 0 : a.n_groups, n_ent = G + a.p.batch;
+  const int G = what == ENT_SEQS ? 0 : a.n_groups;
+  const int n_ent = what == ENT_GROUPS ? G : G + a.p.batch;
   auto ent = [&](int i) {
     return i < G ? att_group_ent(a, i) : att_seq_ent(a, i - G);
   };
+  const AttnSet& set = what == ENT_GROUPS ? a.pre : a.own;
   const int Hkv = a.p.Hkv;
   const PlanStart st =
       plan_start<kNT, M, kBN>(n_ent, Hkv, ent, blockIdx.x, gridDim.x);
-  Body<D, WM> body{a, smem, s_ml, s_bad};
+  Body<D, WM> body{a, set, smem, s_ml, s_bad};
   int64_t x = st.x0, off = st.off, unit0 = st.unit0;
   int e = st.e;
   while (x < st.x1 && e < n_ent) {
@@ -446,7 +452,7 @@ __global__ void __launch_bounds__(kNT)
       const int u = (int)(off / nb), blk = (int)(off - (int64_t)u * nb);
       const int n = (int)min((int64_t)(nb - blk), st.x1 - x);
       const int64_t unit = unit0 + u;
-      if (unit >= a.own.units) {   // q_start or group_start not ascending
+      if (unit >= set.units) {   // q_start or group_start not ascending
         sv_latch(a.p.status, MPK_ERR_INVALID_ARG);
         off = units * nb;
         x = st.x1;
@@ -454,9 +460,9 @@ __global__ void __launch_bounds__(kNT)
       }
       if (blk == 0 && threadIdx.x == 0) {
         const int last = plan_owner(x + nb - 1, st.total, st.n);
-        a.own.meta[unit] =
+        set.meta[unit] =
             make_int2((int)(unit + blockIdx.x), last - (int)blockIdx.x + 1);
-        if (u == 0) a.own.ebase[e] = (int)(unit0 / Hkv);
+        if (u == 0) set.ebase[e] = (int)(unit0 / Hkv);
       }
       body.segment(E, e < G, u / Hkv, u % Hkv, blk, n, unit + blockIdx.x);
       x += n;
@@ -466,7 +472,7 @@ __global__ void __launch_bounds__(kNT)
     unit0 += units;
     ++e;
   }
-  if (a.tc) sv_grid_wait();
+  if (what == ENT_SEQS && a.split != ATT_ONE) sv_grid_wait();
 }
 
 // One warp joins the segments of one (token, query head): the prefix's and
@@ -520,10 +526,11 @@ __global__ void __launch_bounds__(kNT)
   if (a.n_groups > 0) {
     const int g = att_group(a, b);
     const Ent e = att_group_ent(a, g);
-    if (e.k1 > 0) take(a.tc ? a.pre : a.own, g, e.tok0);
+    if (e.k1 > 0) take(a.pre, g, e.tok0);
   }
   const Ent e = att_seq_ent(a, b);
-  if (e.k1 > e.k0) take(a.own, (a.tc ? 0 : a.n_groups) + b, e.tok0);
+  if (e.k1 > e.k0)
+    take(a.own, (a.split == ATT_ONE ? a.n_groups : 0) + b, e.tok0);
   // no key seen: zeros, and -inf for the log sum
   const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
   uint16_t* out = a.out + t * a.out_stride + (int64_t)hq * D + lane * V;
@@ -545,31 +552,33 @@ __global__ void __launch_bounds__(kNT)
 
 int grid_ctas() { return 152 * 2; }
 
-// Row tile by the rows a sequence brings (tokens per sequence on average x
-// heads per KV head): the smallest that holds them, at most 64.
-int own_rows(const AttendArgs& a) {
-  const int64_t rows = (int64_t)a.p.n_tokens * (a.p.Hq / a.p.Hkv);
-  const int64_t per = a.p.batch > 0 ? (rows + a.p.batch - 1) / a.p.batch : 0;
-  const int64_t all = a.n_groups > 0 && !a.tc ? rows / a.n_groups : 0;
-  const int64_t need = per > all ? per : all;
-  return need <= 16 ? 16 : need <= 32 ? 32 : 64;
-}
+// Row tile for entities of `rows` rows: the smallest that holds them, at
+// most 64.
+int row_tile(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 template <int D, int WM>
-cudaError_t run_own(const AttendArgs& a, cudaStream_t s) {
+cudaError_t run_m(const AttendArgs& a, int what, cudaStream_t s) {
   using C = Cfg<D, WM>;
   auto k = attend_kernel<D, WM>;
   cudaError_t e = cudaFuncSetAttribute(
       k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  return sv_launch(k, dim3(grid_ctas()), kNT, C::kSmem, s, true, a);
+  return sv_launch(k, dim3(grid_ctas()), kNT, C::kSmem, s, true, a, what);
+}
+template <int D>
+cudaError_t run(const AttendArgs& a, int M, int what, cudaStream_t s) {
+  return M == 16   ? run_m<D, 1>(a, what, s)
+         : M == 32 ? run_m<D, 2>(a, what, s)
+                   : run_m<D, 4>(a, what, s);
 }
 
 template <int D>
 cudaError_t attend_d(const AttendArgs& a, cudaStream_t s) {
-  cudaError_t e = a.own.M == 16 ? run_own<D, 1>(a, s)
-                  : a.own.M == 32 ? run_own<D, 2>(a, s)
-                                  : run_own<D, 4>(a, s);
+  cudaError_t e = cudaSuccess;
+  if (a.split == ATT_TC) e = launch_attend_tc(a, s);
+  if (a.split == ATT_SPLIT) e = run<D>(a, a.pre.M, ENT_GROUPS, s);
+  if (e != cudaSuccess) return e;
+  e = run<D>(a, a.own.M, a.split == ATT_ONE ? ENT_BOTH : ENT_SEQS, s);
   if (e != cudaSuccess) return e;
   const int64_t warps = (int64_t)a.p.n_tokens * a.p.Hq;
   const int64_t blocks = (warps + kNT / 32 - 1) / (kNT / 32);
@@ -580,6 +589,7 @@ cudaError_t attend_d(const AttendArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+// Chooses the launches and places their results.
 size_t attend_workspace(AttendArgs* a, char* base) {
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -587,21 +597,39 @@ size_t attend_workspace(AttendArgs* a, char* base) {
     off += (bytes + 255) / 256 * 256;
     return p;
   };
-  a->tc = 0;
+  // rows of one KV head, on average over the sequences and over the groups
   const int64_t rows = (int64_t)a->p.n_tokens * (a->p.Hq / a->p.Hkv);
-  a->own.M = own_rows(*a);
-  const int64_t ents = a->p.batch + a->n_groups;
-  // every row is in one sequence's and at most one group's tiles
-  const int64_t tiles = (a->n_groups ? 2 : 1) * (rows / a->own.M) + ents;
-  const int64_t units = tiles * a->p.Hkv, slots = units + grid_ctas();
-  a->own.units = units;
-  a->own.slots = slots;
-  a->own.ebase = reinterpret_cast<int32_t*>(take(ents * 4));
-  a->own.meta = reinterpret_cast<int2*>(take(units * 8));
-  a->own.ml = reinterpret_cast<float2*>(take(slots * a->own.M * 8));
-  a->own.part =
-      reinterpret_cast<float*>(take((size_t)slots * a->own.M * a->p.d * 4));
-  a->pre = a->own;
+  const int64_t per = (rows + a->p.batch - 1) / a->p.batch;
+  const int64_t all = a->n_groups ? rows / a->n_groups : 0;
+  a->own.M = row_tile(per);
+  a->split = ATT_ONE;
+  if (a->n_groups && all > a->own.M) {
+    a->split = ATT_SPLIT;
+    a->pre.M = row_tile(all);
+    if (attend_tc_box(a->p) && a->scale_log2 > 0.f) {
+      a->split = ATT_TC;
+      a->pre.M = attend_tc_rows();
+    }
+  }
+  // a set holds the results of n entities whose rows are disjoint, `times`
+  // over (each row is in one sequence's and at most one group's tiles)
+  auto place = [&](AttnSet* s, int64_t n, int times, int ctas) {
+    s->units = (times * (rows / s->M) + n) * a->p.Hkv;
+    s->slots = s->units + ctas;
+    s->ebase = reinterpret_cast<int32_t*>(take(n * 4));
+    s->meta = reinterpret_cast<int2*>(take(s->units * 8));
+    s->ml = reinterpret_cast<float2*>(take(s->slots * s->M * 8));
+    s->part = reinterpret_cast<float*>(
+        take((size_t)s->slots * s->M * a->p.d * 4));
+  };
+  if (a->split == ATT_ONE) {
+    place(&a->own, a->p.batch + a->n_groups, a->n_groups ? 2 : 1, grid_ctas());
+    a->pre = a->own;
+  } else {
+    place(&a->own, a->p.batch, 1, grid_ctas());
+    place(&a->pre, a->n_groups, 1,
+          a->split == ATT_TC ? attend_tc_ctas() : grid_ctas());
+  }
   return off;
 }
 

@@ -1,0 +1,639 @@
+// Attention over a shared prefix on the 5th-generation tensor cores.
+//
+// Many rows (all tokens of a group, all query heads of a KV head) meet the
+// same keys, so a prefix is a dense product: S = Q K^T, P = e^(S - m),
+// O += P V.  One persistent CTA an SM; a tile is two slots of 128 rows that
+// share every K and V block of 128 keys.
+//
+//   warps 0-3, 4-7  slot 0, slot 1: a thread owns one row.  It loads its row
+//                   of Q, reads its 128 scores from tensor memory, keeps the
+//                   row's maximum and sum in registers, and writes the weights
+//                   back to tensor memory as bf16 over the scores.
+//   warp 8          page lookups and TMA loads of K and V (rings of 2).
+//   warp 9          one thread issues tcgen05.mma: S_i = Q_i K^T (both from
+//                   shared memory), O_i += P_i V (P from tensor memory).
+//
+// While one slot's softmax runs, the tensor core works for the other.  Tensor
+// memory: S (and P) of the slots in columns 0 and 128, O in 256 and 384.
+// O stays there over all key blocks.  It is rescaled only when a row's maximum
+// has grown by more than 2^kSlack over the one its weights are taken to
+// (their ratio cancels in O / l; 2^8 is far from any limit of fp32 or bf16), so
+// nearly every block leaves it alone.
+#include <cuda.h>
+
+#include "attend_plan.cuh"
+
+namespace mpk {
+namespace {
+
+constexpr int kThreadsT = 384;   // two softmax warpgroups, one for the rest
+// Registers move from the third warpgroup to the softmax threads, which hold
+// a row of 128 scores: 2 x 128 x 216 + 128 x 72 = 384 x 168, what the CTA is
+// launched with.
+constexpr int kSoftRegs = 216, kOtherRegs = 72;
+constexpr int kRows = 256;        // rows of a tile
+constexpr int kKeys = 128;        // keys of a block
+constexpr float kSlack = 8.f;
+constexpr uint64_t kWaitNs = 2000000000ull;    // longest wait of a role
+constexpr uint64_t kDrainNs = 200000000ull;    // and for copies at the end
+
+__device__ __forceinline__ uint32_t t_addr(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void bar_init(uint32_t b, uint32_t n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(b) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
+                   b),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(b), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Waits for a phase, for two seconds at most; after that (or when another
+// role has given up) false, and every role leaves its loop.
+__device__ __forceinline__ bool bar_wait(uint32_t b, uint32_t parity,
+                                         volatile int* dead,
+                                         uint64_t limit = kWaitNs) {
+  bool ok = bar_try(b, parity);
+  if (!ok) {
+    uint64_t t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    for (uint32_t i = 1; !ok; ++i) {
+      ok = bar_try(b, parity);
+      if (!ok && (i & 63u) == 0u) {
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        if (*dead || t - t0 > limit) {
+          *dead = 1;
+          break;
+        }
+      }
+    }
+  }
+  // a warp goes on, or leaves, as one
+  return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map,
+                                       int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void tc_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 "
+      "[%0];" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b,
+                                       uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b,
+                                       uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(
+          d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
+        "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+      "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tm_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tm_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ex2t(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Shared-memory operand descriptor: 128-byte swizzled rows (8-row groups of
+// 1024 bytes), groups `stride` bytes apart; `lead` separates the 64-value
+// column panels of an operand whose rows run along the product's inner
+// dimension.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead,
+                                            uint32_t stride) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(lead >> 4) << 16) |
+         ((uint64_t)(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// bf16 x bf16 to fp32, M = 128
+__device__ constexpr uint32_t product(int n, bool b_columns) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_columns ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+template <int D>
+struct TcSmem {
+  static constexpr int kPanels = D / 64;
+  static constexpr int kPanel = 128 * 128;             // 128 rows x 128 bytes
+  static constexpr int kTile = kPanels * kPanel;
+  static constexpr int kQ = 0;                         // [2] tiles
+  static constexpr int kK = 2 * kTile;                 // [2]
+  static constexpr int kV = 4 * kTile;                 // [2]
+  // the output's staging area lies over Q: 8 warps x 32 rows x 36 floats
+  static constexpr int kStage = 32 * 36 * 4;
+  static constexpr int kOver = kTile >= 4 * kStage ? 0 : 1;
+  static constexpr int kExtra = 6 * kTile;             // staging if Q is small
+  static constexpr int kSmem =
+      6 * kTile + (kOver ? 8 * kStage : 0) + 1024;     // + alignment
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsT, 1)
+    attend_tc(const __grid_constant__ AttendArgs a,
+              const __grid_constant__ CUtensorMap mk,
+              const __grid_constant__ CUtensorMap mv, int box) {
+  using L = TcSmem<D>;
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(8) uint64_t bars[20];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_dead;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = (t_addr(raw) + 1023u) & ~1023u;
+  uint8_t* const smem = raw + (base - t_addr(raw));
+  // full / empty of the K and V rings; per slot: Q loaded, scores ready,
+  // weights ready, output complete; the copies of a prefix's last V block
+  const uint32_t b0 = t_addr(bars);
+  const uint32_t k_full = b0, k_empty = b0 + 16, v_full = b0 + 32,
+                 v_empty = b0 + 48, q_full = b0 + 64, s_full = b0 + 80,
+                 p_full = b0 + 96, o_full = b0 + 112, tail = b0 + 128;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      bar_init(k_full + 8 * i, 1);
+      bar_init(k_empty + 8 * i, 1);
+      bar_init(v_full + 8 * i, 1);
+      bar_init(v_empty + 8 * i, 1);
+      bar_init(s_full + 8 * i, 1);
+      bar_init(p_full + 8 * i, 128);
+      bar_init(o_full + 8 * i, 1);
+      bar_init(q_full + 8 * i, 128);
+    }
+    bar_init(tail, 1);
+    s_dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile(
+        "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::
+            "r"(t_addr(&s_tmem))
+        : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::
+                     : "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tm = s_tmem;
+  sv_grid_wait();
+  // everything before this kernel is complete: the next one may start
+  sv_grid_launch();
+  const PagedArgs& p = a.p;
+  const int Hkv = p.Hkv, grp = p.Hq / p.Hkv;
+  const PlanStart st = plan_start<kThreadsT, kRows, kKeys>(
+      a.n_groups, Hkv, [&](int g) { return att_group_ent(a, g); }, blockIdx.x,
+      gridDim.x);
+  volatile int* dead = &s_dead;
+
+  // All roles walk the same segments.  f(E, tile, h, blk, n, slot, two):
+  // `two`: the tile has rows in its second slot.  f returns false to stop.
+  auto walk = [&](bool writes_meta, auto f) {
+    int64_t x = st.x0, off = st.off, unit0 = st.unit0;
+    for (int e = st.e; x < st.x1 && e < a.n_groups; ++e, off = 0) {
+      const Ent E = att_group_ent(a, e);
+      const int nb = (E.k1 - E.k0 + kKeys - 1) / kKeys;
+      const int64_t units =
+          nb > 0 ? (int64_t)((E.rows + kRows - 1) / kRows) * Hkv : 0;
+      while (x < st.x1 && off < units * nb) {
+        const int u = (int)(off / nb), blk = (int)(off - (int64_t)u * nb);
+        const int n = (int)min((int64_t)(nb - blk), st.x1 - x);
+        const int64_t unit = unit0 + u;
+        if (unit >= a.pre.units) {   // q_start or group_start not ascending
+          sv_latch(p.status, MPK_ERR_INVALID_ARG);
+          return;
+        }
+        if (writes_meta && blk == 0) {
+          const int last = plan_owner(x + nb - 1, st.total, st.n);
+          a.pre.meta[unit] =
+              make_int2((int)(unit + blockIdx.x), last - (int)blockIdx.x + 1);
+          if (u == 0) a.pre.ebase[e] = (int)(unit0 / Hkv);
+        }
+        const int tile = u / Hkv;
+        if (!f(E, tile, u % Hkv, blk, n, unit + blockIdx.x,
+               E.rows > tile * kRows + 128))
+          return;
+        x += n;
+        off += n;
+      }
+      unit0 += units;
+    }
+  };
+
+  if (warp >= 8) {
+    // (warps 10 and 11 fill up the warpgroup)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8) {
+    // ---------------------------------------------------------- loads
+    int it = 0, sent[2] = {0, 0};
+    uint32_t tail_ph = 0;
+    walk(lane == 0, [&](const Ent& E, int, int h, int blk, int n, int64_t,
+                        bool) {
+      const int32_t* pt = p.page_table + (int64_t)E.seq * p.max_pages;
+      for (int j = 0; j < n; ++j, ++it) {
+        const int st_ = it & 1;
+        const uint32_t ph = (uint32_t)((it >> 1) & 1);
+        const int key0 = (blk + j) * kKeys;
+        // lane i finds the page of box i
+        const int t = key0 + lane * box;
+        int row = -1;
+        if (lane < kKeys / box && t < E.k1) {
+          const int pi = (int)sv_div(t, p.page_div);
+          const int page = __ldg(pt + pi);
+          if (page >= 0 && page < p.num_pages)
+            row = (page * Hkv + h) * p.page_size + (t - pi * p.page_size);
+          else
+            sv_latch(p.status, MPK_ERR_KV_PAGE);
+        }
+        const int boxes = __popc(__ballot_sync(0xffffffffu, row >= 0));
+        const uint32_t bytes = (uint32_t)boxes * box * D * 2;
+        const bool last = key0 + kKeys > E.k1;
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t empty = (kv ? v_empty : k_empty) + 8 * st_;
+          uint32_t full = (kv ? v_full : k_full) + 8 * st_;
+          const uint32_t dst =
+              base + (kv ? L::kV : L::kK) + st_ * L::kTile;
+          if (!bar_wait(empty, ph ^ 1u, dead)) return false;
+          const bool fill = kv && last;
+          const uint32_t bar = fill ? tail : full;
+          if (lane == 0) bar_expect(bar, bytes);
+          if (!fill) sent[kv] = it + 1;
+          __syncwarp();
+          if (row >= 0)
+#pragma unroll
+            for (int q = 0; q < L::kPanels; ++q)
+              tma_2d(dst + q * L::kPanel + lane * box * 128, kv ? &mv : &mk,
+                     q * 64, row, bar);
+          if (fill) {
+            // values of keys past the end: zeros, because a weight of 0
+            // times whatever the page holds there need not be 0
+            if (!bar_wait(tail, tail_ph, dead)) return false;
+            tail_ph ^= 1u;
+            uint8_t* v = smem + L::kV + st_ * L::kTile;
+            const int r0 = E.k1 - key0;
+            for (int i = lane; i < (kKeys - r0) * 8; i += 32)
+#pragma unroll
+              for (int q = 0; q < L::kPanels; ++q)
+                *reinterpret_cast<uint4*>(v + q * L::kPanel +
+                                          (r0 + i / 8) * 128 + (i % 8) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            fence_async();
+            __syncwarp();
+            if (lane == 0) bar_arrive(full);
+          }
+        }
+      }
+      return true;
+    });
+    // no copy may land after the CTA has left, nor the tensor core's arrivals
+    // for the last two blocks
+    int late = 0;
+    for (int kv = 0; kv < 2; ++kv)
+      for (int k = sent[kv] - 2; k < sent[kv]; ++k)
+        if (k >= 0)
+          bar_wait((kv ? v_full : k_full) + 8 * (k & 1), (k >> 1) & 1, &late,
+                   kDrainNs);
+    for (int k = it - 2; k < it; ++k)
+      if (k >= 0 && !*dead) {
+        bar_wait(k_empty + 8 * (k & 1), (k >> 1) & 1, dead);
+        bar_wait(v_empty + 8 * (k & 1), (k >> 1) & 1, dead);
+      }
+    } else if (warp == 9) {
+    // ------------------------------------------------------- products
+    constexpr uint32_t iqk = product(kKeys, false), ipv = product(D, true);
+    int it = 0;
+    uint32_t pn[2] = {0, 0}, qn[2] = {0, 0};
+    auto qk = [&](int i, int stage) {
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t o = (k / 4) * L::kPanel + (k % 4) * 32;
+          mma_ss(tm + 128 * i,
+                 operand(base + L::kQ + i * L::kTile + o, 16, 1024),
+                 operand(base + L::kK + stage * L::kTile + o, 16, 1024), iqk,
+                 k > 0);
+        }
+        tc_commit(s_full + 8 * i);
+      }
+    };
+    walk(false, [&](const Ent&, int, int, int, int n, int64_t, bool two) {
+      for (int i = 0; i < (two ? 2 : 1); ++i) {
+        if (!bar_wait(q_full + 8 * i, qn[i] & 1, dead)) return false;
+        ++qn[i];
+      }
+      if (!bar_wait(k_full + 8 * (it & 1), (it >> 1) & 1, dead)) return false;
+      tc_after();
+      qk(0, it & 1);
+      if (two) qk(1, it & 1);
+      if (lane == 0) tc_commit(k_empty + 8 * (it & 1));
+      for (int j = 0; j < n; ++j, ++it) {
+        const int sv = it & 1, sk = (it + 1) & 1;
+        if (!bar_wait(v_full + 8 * sv, (it >> 1) & 1, dead)) return false;
+        const bool more = j + 1 < n;
+        if (more && !bar_wait(k_full + 8 * sk, ((it + 1) >> 1) & 1, dead))
+          return false;
+        for (int i = 0; i < (two ? 2 : 1); ++i) {
+          if (!bar_wait(p_full + 8 * i, pn[i] & 1, dead)) return false;
+          ++pn[i];
+          tc_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_ts(tm + 256 + 128 * i, tm + 128 * i + 8 * k,
+                     operand(base + L::kV + sv * L::kTile + k * 2048,
+                             L::kPanel, 1024),
+                     ipv, j > 0 || k > 0);
+            if (!more) tc_commit(o_full + 8 * i);
+          }
+          if (more) qk(i, sk);
+        }
+        if (lane == 0) {
+          tc_commit(v_empty + 8 * sv);
+          if (more) tc_commit(k_empty + 8 * sk);
+        }
+        __syncwarp();
+      }
+      return true;
+    });
+    }
+  } else {
+    // -------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    const int slot = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // 32 lanes a warp
+    const uint32_t tS = tm + lanes + 128 * slot, tO = tS + 256;
+    uint32_t sn = 0, on = 0;
+    walk(false, [&](const Ent& E, int tile, int h, int blk, int n,
+                    int64_t part_slot, bool two) {
+      if (slot == 1 && !two) return true;
+      {
+        // this thread's row of Q, swizzled as the tensor core expects
+        const int row = tile * kRows + slot * 128 + r;
+        uint8_t* q = smem + L::kQ + slot * L::kTile;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + (E.tok0 + (row < E.rows ? row / grp : 0)) * a.q_stride +
+            (int64_t)(h * grp + (row < E.rows ? row % grp : 0)) * D);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 u =
+              row < E.rows ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(q + (c / 8) * L::kPanel + r * 128 +
+                                    (((c & 7) ^ (r & 7)) << 4)) = u;
+        }
+      }
+      fence_async();
+      bar_arrive(q_full + 8 * slot);
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j) {
+        if (!bar_wait(s_full + 8 * slot, sn & 1, dead)) return false;
+        ++sn;
+        tc_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tm_ld32(tS + 32 * c, s + 32 * c);
+        tm_wait_ld();
+        const int valid = E.k1 - (blk + j) * kKeys;
+        if (valid < kKeys) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= valid) s[c] = 0xff800000u;
+        }
+        float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) {
+          t0 = fmaxf(t0, fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
+          t1 = fmaxf(t1, fmaxf(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])));
+          t2 = fmaxf(t2, fmaxf(__uint_as_float(s[c + 4]), __uint_as_float(s[c + 5])));
+          t3 = fmaxf(t3, fmaxf(__uint_as_float(s[c + 6]), __uint_as_float(s[c + 7])));
+        }
+        const float top =
+            fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * a.scale_log2;
+        const bool grow = top > m + kSlack || m == -INFINITY;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float mn = grow ? fmaxf(m, top) : m;
+          const float f = m == -INFINITY ? 0.f : ex2t(m - mn);
+          l *= f;
+          m = mn;
+          if (j > 0) {
+            // S of this block was committed behind the product before, so
+            // O is at rest
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tm_ld32(tO + 32 * c, o);
+              tm_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tm_st32(tO + 32 * c, o);
+            }
+          }
+        }
+        const float neg = m == -INFINITY ? 0.f : -m;
+        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float p0 = ex2t(fmaf(__uint_as_float(s[64 * c + 2 * i]),
+                                       a.scale_log2, neg));
+            const float p1 = ex2t(fmaf(__uint_as_float(s[64 * c + 2 * i + 1]),
+                                       a.scale_log2, neg));
+            const float p2 = ex2t(fmaf(__uint_as_float(s[64 * c + 2 * i + 2]),
+                                       a.scale_log2, neg));
+            const float p3 = ex2t(fmaf(__uint_as_float(s[64 * c + 2 * i + 3]),
+                                       a.scale_log2, neg));
+            l0 += p0;
+            l1 += p1;
+            l2 += p2;
+            l3 += p3;
+            // rounded to bf16 as in attend.cu; the sum takes them unrounded
+            w[i] = sv_pack(p0, p1);
+            w[i + 1] = sv_pack(p2, p3);
+          }
+          tm_st32(tS + 32 * c, w);
+        }
+        l += (l0 + l1) + (l2 + l3);
+        tm_wait_st();
+        tc_before();
+        bar_arrive(p_full + 8 * slot);
+      }
+      // ---- the segment's result
+      if (!bar_wait(o_full + 8 * slot, on & 1, dead)) return false;
+      ++on;
+      tc_after();
+      const int64_t at = part_slot * kRows + slot * 128;
+      a.pre.ml[at + r] = make_float2(m, l);
+      float* out = a.pre.part + (at + (warp & 3) * 32) * D;
+      float* stage = reinterpret_cast<float*>(
+          smem + (L::kOver ? L::kExtra + warp * L::kStage
+                           : L::kQ + slot * L::kTile + (warp & 3) * L::kStage));
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tm_ld32(tO + 32 * c, o);
+        tm_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(stage + lane * 36 + 4 * i) =
+              make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = i * 4 + (lane >> 3);
+          *reinterpret_cast<float4*>(out + rr * D + 32 * c + 4 * (lane & 7)) =
+              *reinterpret_cast<const float4*>(stage + rr * 36 +
+                                               4 * (lane & 7));
+        }
+        __syncwarp();
+      }
+      tc_before();
+      return true;
+    });
+  }
+  __syncthreads();
+  if (tid == 0 && s_dead) sv_latch(p.status, MPK_ERR_TIMEOUT);
+  if (warp == 8) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(
+        tm));
+  }
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
+                             void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*,
+                             CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Pages as rows of d values, in boxes of `box` rows x 64 values.
+bool page_map(EncodeFn fn, const PagedArgs& p, const void* pool, int box,
+              CUtensorMap* m) {
+  const cuuint64_t dims[2] = {
+      (cuuint64_t)p.d, (cuuint64_t)p.num_pages * p.Hkv * p.page_size};
+  const cuuint64_t strides[1] = {(cuuint64_t)p.d * 2};
+  const cuuint32_t boxes[2] = {64, (cuuint32_t)box};
+  const cuuint32_t steps[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool),
+            dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t tc_d(const AttendArgs& a, const CUtensorMap& mk,
+                 const CUtensorMap& mv, int box, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(
+      attend_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      TcSmem<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  return sv_launch(attend_tc<D>, dim3(attend_tc_ctas()), kThreadsT,
+                   TcSmem<D>::kSmem, s, true, a, mk, mv, box);
+}
+
+}  // namespace
+
+int attend_tc_ctas() { return 152; }
+int attend_tc_rows() { return kRows; }
+
+// Rows of a page that one TMA box takes: a power of two (so that blocks of
+// 128 keys are whole boxes) that divides the page; 0 when that is below the 8
+// rows of a swizzle group, or the head or the pool does not fit.
+int attend_tc_box(const PagedArgs& p) {
+  if (p.d != 64 && p.d != 128) return 0;
+  if ((int64_t)p.num_pages * p.Hkv * p.page_size > 0x7fffffff) return 0;
+  int box = p.page_size & -p.page_size;
+  if (box > 128) box = 128;
+  return box < 8 ? 0 : box;
+}
+
+cudaError_t launch_attend_tc(const AttendArgs& a, cudaStream_t s) {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                         cudaEnableDefault, &r) !=
+            cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  const int box = attend_tc_box(a.p);
+  CUtensorMap mk, mv;
+  if (!fn || !box || !page_map(fn, a.p, a.p.k, box, &mk) ||
+      !page_map(fn, a.p, a.p.v, box, &mv))
+    return cudaErrorNotSupported;
+  return a.p.d == 128 ? tc_d<128>(a, mk, mv, box, s)
+                      : tc_d<64>(a, mk, mv, box, s);
+}
+
+}  // namespace mpk

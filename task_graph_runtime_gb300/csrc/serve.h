@@ -77,9 +77,18 @@ struct AttendArgs {
   uint16_t* out;
   int64_t out_stride;
   float* lse;                  // nullable [n_tokens][Hq]
-  AttnSet own, pre;            // own: sequences (and groups if !tc)
-  int tc;                      // prefixes by the tensor-memory kernel
+  AttnSet own, pre;            // results of the sequences, of the groups
+  int split;                   // ATT_*: who attends to the prefixes
 };
+enum {
+  ATT_ONE = 0,                 // one launch does both (pre is own then)
+  ATT_SPLIT = 1,               // a launch of their own, with larger row tiles
+  ATT_TC = 2                   // the tensor-memory kernel
+};
+int attend_tc_ctas();
+int attend_tc_rows();
+int attend_tc_box(const PagedArgs& p);
+cudaError_t launch_attend_tc(const AttendArgs& a, cudaStream_t s);
 // Workspace bytes, and the pointers of *a into it (base may be null).
 size_t attend_workspace(AttendArgs* a, char* base);
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s);

@@ -176,7 +176,13 @@ size_t mpk_prefix_attention_workspace(const mpk_attn_shape* shape,
   a.p.d = shape->head_dim;
   a.n_groups = n_groups;
   if (attend_too_large(a.p)) return 0;
-  return attend_workspace(&a, nullptr);
+  // enough for whichever launches the call chooses
+  a.scale_log2 = 1.f;
+  a.p.num_pages = 1;
+  const size_t x = attend_workspace(&a, nullptr);
+  a.scale_log2 = -1.f;
+  const size_t y = attend_workspace(&a, nullptr);
+  return x > y ? x : y;
 }
 
 mpk_status mpk_prefix_attention(const mpk_attn_shape* shape,
@@ -205,6 +211,9 @@ mpk_status mpk_prefix_attention(const mpk_attn_shape* shape,
     a.prefix_len = groups->prefix_len;
   }
   if (attend_too_large(a.p)) return MPK_ERR_UNSUPPORTED;
+  const double s = scale != 0.f ? (double)scale
+                                : 1.0 / std::sqrt((double)a.p.d);
+  a.scale_log2 = (float)(s * 1.4426950408889634074);
   if (!d_workspace || off(d_workspace, 256) ||
       workspace_bytes < attend_workspace(&a, static_cast<char*>(d_workspace)))
     return MPK_ERR_INVALID_ARG;
@@ -213,9 +222,6 @@ mpk_status mpk_prefix_attention(const mpk_attn_shape* shape,
   a.out = static_cast<uint16_t*>(d_out);
   a.out_stride = out_stride;
   a.lse = d_lse;
-  const double s = scale != 0.f ? (double)scale
-                                : 1.0 / std::sqrt((double)a.p.d);
-  a.scale_log2 = (float)(s * 1.4426950408889634074);
   return from_cuda(launch_attend(a, static_cast<cudaStream_t>(cuda_stream)));
 }
 

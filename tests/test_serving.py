@@ -285,6 +285,86 @@ ATTEND = {
                  groups=([0, 50, 150], [0, 147])),
 }
 
+# groups with more rows than a sequence: the prefix has launches of its own
+PREFIX = {
+    "one_block": dict(n=[1] * 20, ctx=[100] * 20, d=128, hq=8,
+                      groups=([0, 20], [100])),
+    "two_slots": dict(n=[1] * 50, ctx=[130] * 50, d=128, hq=8,
+                      groups=([0, 50], [128])),
+    "tiles": dict(n=[2] * 90, ctx=[300] * 90, d=128, hq=8,
+                  groups=([0, 90], [257])),
+    "d64": dict(n=[1] * 40, ctx=[270] * 40, d=64, hq=16, hkv=2, page=8,
+                groups=([0, 40], [270])),
+    "page24": dict(n=[1, 4] * 10, ctx=[205] * 20, d=64, page=24,
+                   groups=([0, 20], [201])),
+    "page128": dict(n=[3] * 12, ctx=[1000] * 12, d=128, page=128,
+                    groups=([0, 12], [999])),
+    "page64_long": dict(n=[1] * 16, ctx=[5000] * 16, d=128, page=64, hq=8,
+                        hkv=2, groups=([0, 16], [4999])),
+    "page100": dict(n=[1] * 16, ctx=[205] * 16, d=64, page=100, hq=8,
+                    groups=([0, 16], [201])),
+    "d32": dict(n=[1] * 16, ctx=[205] * 16, d=32, hq=8,
+                groups=([0, 16], [201])),
+    "several": dict(n=[1, 5, 0] * 20, ctx=[300 + i for i in range(60)], d=64,
+                    hq=12, hkv=4, groups=([0, 7, 8, 33, 60],
+                                          [300, 0, 1, 129]), pad=5),
+}
+
+
+@gpu
+@pytest.mark.parametrize("name", sorted(PREFIX))
+def test_attend_prefix_launches(name):
+    c = Case(41, **PREFIX[name])
+    out, lse = c.attend()
+    assert c.status.item() == 0
+    c.check(out, lse)
+    again, la = c.attend()
+    assert torch.equal(out, again) and torch.equal(lse, la)
+
+
+@gpu
+@pytest.mark.parametrize("name", ["tiles", "d64", "page100"])
+@pytest.mark.parametrize("stale", [math.nan, -math.inf])
+def test_attend_prefix_launches_stale_slots(name, stale):
+    c = Case(42, stale=stale, **PREFIX[name])
+    out, lse = c.attend()
+    c.check(out, lse)
+    assert torch.isfinite(out[:c.T].float()).all()
+
+
+@gpu
+@pytest.mark.parametrize("scale", [2.0, -0.3])
+def test_attend_prefix_launches_scale(scale):
+    # large scores: the running maximum grows often; a negative scale
+    c = Case(43, **PREFIX["page64_long"])
+    out, lse = c.attend(scale=scale)
+    c.check(out, lse, scale)
+
+
+@gpu
+def test_attend_prefix_launches_growing_maximum():
+    # keys that grow along the prefix: every block raises the maximum
+    c = Case(44, **PREFIX["tiles"])
+    t = torch.arange(300, device="cuda").float().div(40)
+    for b in [0]:
+        row = torch.from_numpy(c.table[b].astype(np.int64)).cuda()
+        pg, sl = row[torch.arange(300).cuda() // 16], torch.arange(300) % 16
+        k = c.k[c.layer, pg, :, sl].float() * t[:, None, None]
+        c.k[c.layer, pg, :, sl] = k.bfloat16()
+    out, lse = c.attend()
+    c.check(out, lse)
+
+
+@gpu
+def test_attend_prefix_launches_missing_page():
+    c = Case(45, n=[1] * 40, ctx=[200] * 40, d=128, hq=8,
+             groups=([0, 20, 40], [128, 128]))
+    want, _ = c.attend()
+    c.kv.page_table[0, 3] = -1
+    out, _ = c.attend()
+    assert c.status.item() == mpk.MPK_ERR_KV_PAGE
+    assert torch.equal(out[20:], want[20:])
+
 
 @gpu
 @pytest.mark.parametrize("name", sorted(ATTEND))
