@@ -17,7 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libmpk.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 # the serving operators' kernels
-SERVE = ["append", "attend", "attend_tc", "verify"]
+SERVE = ["append", "attend", "attend_d32", "attend_d64", "attend_d128",
+         "attend_tc", "verify"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

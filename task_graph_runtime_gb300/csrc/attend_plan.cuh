@@ -3,7 +3,8 @@
 //
 // Entities are the groups (a prefix and the rows of all its sequences) and
 // then the sequences (own keys and own rows).  An entity's rows are cut into
-// tiles of M, its keys into blocks of BN; a unit is one (row tile, KV head).
+// tiles of MP (groups) or MO (sequences), its keys into blocks of BN; a unit
+// is one (row tile, KV head), numbered among the groups' or the sequences'.
 // All blocks of all units form one line, of which every CTA takes an equal
 // stretch: the load is even whatever the lengths are, and a long key axis is
 // split when there are few rows.  A stretch of one unit's blocks is a
@@ -83,17 +84,17 @@ struct PlanStart {
   int64_t x0, x1;      // this CTA's stretch
   int64_t total;       // blocks of all units
   int64_t off;         // x0 within entity e
-  int64_t unit0;       // units before entity e
+  int unit0;           // units before entity e, of its kind
   int e;
   int n;               // CTAs that take part
 };
 
 // Finds the CTA's stretch with one scan over the entities (NT threads).
 // Both passes of a batch of more than NT entities read the arrays again.
-// `ent(e)` gives entity e.
-template <int NT, int M, int BN, typename F>
-__device__ __forceinline__ PlanStart plan_start(int n_ent, int Hkv, F ent,
-                                                int cta, int n_cta) {
+// `ent(e)` gives entity e; the first G are groups.
+template <int NT, int MP, int MO, int BN, typename F>
+__device__ __forceinline__ PlanStart plan_start(int G, int n_ent, int Hkv,
+                                                F ent, int cta, int n_cta) {
   __shared__ int64_t sh_cost[NT / 32], sh_unit[NT / 32];
   __shared__ int64_t sh_off, sh_base;
   __shared__ int sh_e;
@@ -103,9 +104,12 @@ __device__ __forceinline__ PlanStart plan_start(int n_ent, int Hkv, F ent,
     if (i < n_ent) {
       const Ent e = ent(i);
       const int64_t nb = (e.k1 - e.k0 + BN - 1) / BN;
-      const int64_t nt = (e.rows + M - 1) / M;
+      const int64_t nt =
+          i < G ? (e.rows + MP - 1) / MP : (e.rows + MO - 1) / MO;
       cost = nb * nt * Hkv;
+      // groups in the low half, sequences in the high half
       unit = nb > 0 ? nt * Hkv : 0;
+      if (i >= G) unit <<= 32;
     }
   };
   int64_t cost, unit, total = 0;
@@ -173,7 +177,7 @@ __device__ __forceinline__ PlanStart plan_start(int n_ent, int Hkv, F ent,
   __syncthreads();
   st.e = sh_e;
   st.off = sh_off;
-  st.unit0 = sh_base;
+  st.unit0 = (int)(st.e < G ? sh_base : sh_base >> 32);
   return st;
 }
 

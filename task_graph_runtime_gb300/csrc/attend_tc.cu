@@ -249,8 +249,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   sv_grid_launch();
   const PagedArgs& p = a.p;
   const int Hkv = p.Hkv, grp = p.Hq / p.Hkv;
-  const PlanStart st = plan_start<kThreadsT, kRows, kKeys>(
-      a.n_groups, Hkv, [&](int g) { return att_group_ent(a, g); }, blockIdx.x,
+  const PlanStart st = plan_start<kThreadsT, kRows, kRows, kKeys>(
+      a.n_groups, a.n_groups, Hkv, [&](int g) { return att_group_ent(a, g); }, blockIdx.x,
       gridDim.x);
   volatile int* dead = &s_dead;
 
@@ -318,14 +318,14 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         const bool last = key0 + kKeys > E.k1;
         for (int kv = 0; kv < 2; ++kv) {
           const uint32_t empty = (kv ? v_empty : k_empty) + 8 * st_;
-          uint32_t full = (kv ? v_full : k_full) + 8 * st_;
+          const uint32_t full = (kv ? v_full : k_full) + 8 * st_;
           const uint32_t dst =
               base + (kv ? L::kV : L::kK) + st_ * L::kTile;
           if (!bar_wait(empty, ph ^ 1u, dead)) return false;
           const bool fill = kv && last;
           const uint32_t bar = fill ? tail : full;
           if (lane == 0) bar_expect(bar, bytes);
-          if (!fill) sent[kv] = it + 1;
+          if (!fill) sent[kv] = it + 1;   // `full` will be reached
           __syncwarp();
           if (row >= 0)
 #pragma unroll
@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             fence_async();
             __syncwarp();
             if (lane == 0) bar_arrive(full);
+            sent[kv] = it + 1;
           }
         }
       }

@@ -78,13 +78,14 @@ struct AttendArgs {
   int64_t out_stride;
   float* lse;                  // nullable [n_tokens][Hq]
   AttnSet own, pre;            // results of the sequences, of the groups
-  int split;                   // ATT_*: who attends to the prefixes
+  int tc;                      // prefixes by the tensor-memory kernel
+  int wmp, wmo;                // row tiles of attend_kernel (16 x these)
 };
-enum {
-  ATT_ONE = 0,                 // one launch does both (pre is own then)
-  ATT_SPLIT = 1,               // a launch of their own, with larger row tiles
-  ATT_TC = 2                   // the tensor-memory kernel
-};
+int attend_ctas();
+// the general kernel, one translation unit per head_dim
+cudaError_t launch_attend_32(const AttendArgs& a, cudaStream_t s);
+cudaError_t launch_attend_64(const AttendArgs& a, cudaStream_t s);
+cudaError_t launch_attend_128(const AttendArgs& a, cudaStream_t s);
 int attend_tc_ctas();
 int attend_tc_rows();
 int attend_tc_box(const PagedArgs& p);
