@@ -140,7 +140,8 @@ cudaError_t run_merge(const AttendArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int attend_ctas() { return 152 * 2; }
+// at most: one CTA for each of four places on 152 SMs
+int attend_ctas() { return 152 * 4; }
 
 // Chooses the launches and places their results.
 size_t attend_workspace(AttendArgs* a, char* base) {
@@ -156,8 +157,8 @@ size_t attend_workspace(AttendArgs* a, char* base) {
   const int64_t all = a->n_groups ? (rows + a->n_groups - 1) / a->n_groups : 0;
   // the smallest row tiles that hold them; few pairs are built
   a->wmo = per <= 16 ? 1 : per <= 32 ? 2 : 4;
-  a->wmp = a->wmo > 1 || all > 16 ? 4 : 1;
   a->tc = all > 64 && attend_tc_box(a->p) && a->scale_log2 > 0.f;
+  a->wmp = a->wmo > 1 || (all > 16 && !a->tc) ? 4 : 1;
   a->own.M = 16 * a->wmo;
   a->pre.M = a->tc ? attend_tc_rows() : 16 * a->wmp;
   // a set holds the results of n entities whose rows are disjoint

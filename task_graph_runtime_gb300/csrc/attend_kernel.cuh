@@ -14,12 +14,14 @@
 // sequence's 16 WMO.  A warp holds 16 rows and 64 / (4 / WM) keys of a block
 // of 64; mma.sync m16n8k16, scores and weights stay in registers.  With few
 // rows the warps split the keys, so that the tensor instructions per block
-// stay few; the kernel is bound by the K/V bytes.  Blocks come through a ring
-// of kStages shared-memory stages, 16-byte asynchronous copies, every token
-// from its own page (any page size).  The copies run ahead over the whole
-// stretch of the CTA, across the ends of segments, and the next segment's
-// queries are fetched during the last block of the one before, so a stretch
-// of many short sequences streams like one long one.
+// stay few; the kernel is bound by the K/V bytes.
+// A fifth warp walks the stretch ahead of them: it looks up the pages (any
+// page size, one block early), copies K, V and the queries of a 16-row tile
+// into a ring of kStages shared-memory stages (16-byte asynchronous copies
+// that arrive on the stage's barrier), and leaves a description of the block
+// there.  The others touch no list, table or length, and a stretch of many
+// short sequences streams like one long one: the chain lengths -> pages ->
+// keys that starts a sequence runs while earlier blocks are computed.
 #pragma once
 
 #include "attend_plan.cuh"
@@ -27,25 +29,27 @@
 namespace mpk {
 namespace {
 
-constexpr int kNT = 128;
+constexpr int kNT = 160;       // four warps that compute, one that copies
+constexpr int kComp = 128;
 constexpr int kBN = 64;
-constexpr int kStages = 3;
+constexpr float kSlack = 8.f;
 
-__device__ __forceinline__ uint32_t s_addr(const void* p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
 // 16 bytes, or zeros when n == 0 (nothing is read then)
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int n) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
                "l"(src), "r"(n)
                : "memory");
 }
-__device__ __forceinline__ void cp_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
+// an arrival on `bar` once this thread's copies so far have landed
+__device__ __forceinline__ void cp_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar)
+               : "memory");
 }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void cp_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+__device__ __forceinline__ void sync_threads(int id, int n) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 __device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile(
@@ -84,17 +88,32 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return r * (D * 2) + ((c ^ (r & 7)) << 4);
 }
 
+// What the copying warp says of the block in a stage.
+struct Blk {
+  int k1, key;         // end of the unit's keys, first key of the block
+  int tok0, rows;      // its entity's first token row and rows
+  int tile, h;         // row tile, KV head
+  int unit;
+  int flags;           // BLK_*
+};
+enum { BLK_PREFIX = 1, BLK_FIRST = 2, BLK_LAST = 4, BLK_STOP = 8 };
+
 template <int D>
 struct Cfg {
+  // CTAs an SM and stages a CTA: the consumers' registers allow two or three
+  // CTAs; the stages fill the shared memory that they share.
+  static constexpr int kCtas = D == 128 ? 2 : 3;
+  static constexpr int kStages = D == 128 ? 3 : 4;
   static constexpr int kTile = kBN * D * 2;            // bytes of K (or V)
-  static constexpr int kStage = 2 * kTile;
+  static constexpr int kQ = 16 * D * 2;                // queries of 16 rows
+  static constexpr int kStage = 2 * kTile + kQ;
   static constexpr int kSmem = kStages * kStage;
   static constexpr int CH = D / 8;                     // chunks a row
   static constexpr int kPitch = D + 4;                 // merge buffer, floats
   // rows that the merge of four key slices takes at a time (it lies over a
   // stage that has been consumed)
   static constexpr int kPass = 8;
-  static_assert(4 * kPass * kPitch * 4 <= kStage, "merge buffer");
+  static_assert(4 * kPass * kPitch * 4 <= 2 * kTile, "merge buffer");
 };
 
 // A position on the CTA's stretch of the line.
@@ -104,29 +123,17 @@ struct Cursor {
   int64_t left;        // blocks of the stretch from here on
 };
 
-// What the blocks of a segment need to know.
-struct Seg {
-  int k1, key;         // end of the keys; first key of the next block
-  int lim[2], lim_min; // keys this thread's two rows see
-  bool prefix;
-};
-
+// The copying warp.
 template <int D, int WMP, int WMO>
-struct Attend {
+struct Copier {
   using C = Cfg<D>;
   static constexpr int CH = C::CH;
-  static constexpr int RPT = kBN * CH / kNT;           // rows a thread loads
-  static constexpr int RSTEP = kNT / CH;
-
   const AttendArgs& a;
   uint8_t* smem;
-  float (*s_ml)[2];    // [4 * 16] of each warp's rows
-  uint32_t* s_bad;     // [2] keys of a block whose V is not finite
+  Blk* blk;
+  uint32_t full, empty;
+  volatile int* dead;
   int G, n_ent;
-
-  uint32_t qf[D / 16][4];
-  float o[D / 8][4];
-  float m[2], l[2];
 
   __device__ __forceinline__ Ent ent(int i) const {
     return i < G ? att_group_ent(a, i) : att_seq_ent(a, i - G);
@@ -154,57 +161,171 @@ struct Attend {
     } while (c.units == 0);
     c.u = 0;
   }
-
-  // K and V of the cursor's block into stage st
-  __device__ __forceinline__ void load(const Cursor& cu, int st) {
-    const PagedArgs& p = a.p;
-    const uint32_t ks = s_addr(smem + st * C::kStage);
-    const int c = threadIdx.x % CH, r0 = threadIdx.x / CH;
-    const int h = cu.u % p.Hkv, key = cu.E.k0 + cu.blk * kBN;
-    const int32_t* pt = p.page_table + (int64_t)cu.E.seq * p.max_pages;
-    int pi[RPT], page[RPT];
+  // Lane i looks up the pages of keys i and i + 32 of the cursor's block; -2
+  // for keys past the end.
+  __device__ __forceinline__ void pages(const Cursor& c, int (&pg)[2]) const {
+    const int lane = threadIdx.x & 31;
+    const int32_t* pt = a.p.page_table + (int64_t)c.E.seq * a.p.max_pages;
 #pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-      const int t = key + r0 + i * RSTEP;
-      pi[i] = (int)sv_div(t, p.page_div);
-      page[i] = t < cu.E.k1 ? __ldg(pt + pi[i]) : -2;
-    }
-#pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-      const int r = r0 + i * RSTEP, t = key + r;
-      const bool ok = page[i] >= 0 && page[i] < p.num_pages;
-      if (!ok && page[i] != -2) sv_latch(p.status, MPK_ERR_KV_PAGE);
-      const int64_t off =
-          ok ? (((int64_t)page[i] * p.Hkv + h) * p.page_size +
-                (t - pi[i] * p.page_size)) * D + c * 8
-             : 0;
-      const uint32_t dst = ks + swz<D>(r, c);
-      cp16(dst, p.k + off, ok ? 16 : 0);
-      cp16(dst + C::kTile, p.v + off, ok ? 16 : 0);
+    for (int i = 0; i < 2; ++i) {
+      const int t = c.E.k0 + c.blk * kBN + lane + 32 * i;
+      pg[i] = t < c.E.k1 ? __ldg(pt + sv_div(t, a.p.page_div)) : -2;
     }
   }
 
-  // This thread's part of the queries of the cursor's unit, in the layout of
-  // the product's first operand (rows past the entity's are zeros).
-  template <int WM>
-  __device__ __forceinline__ void queries(const Cursor& cu,
-                                          uint32_t (&q)[D / 16][4]) {
+  __device__ __forceinline__ void run(const PlanStart& ps) {
     const PagedArgs& p = a.p;
+    const int lane = threadIdx.x & 31;
+    const int grp = p.Hq / p.Hkv;
+    Cursor c;
+    c.e = ps.e;
+    c.unit0 = ps.unit0;
+    c.left = ps.x1 - ps.x0;
+    enter(c);
+    c.u = (int)(ps.off / c.nb);
+    c.blk = (int)(ps.off - (int64_t)c.u * c.nb);
+    const int64_t dv = reinterpret_cast<const char*>(p.v) -
+                       reinterpret_cast<const char*>(p.k);
+    const int ch = lane % CH, r0 = lane / CH;
+    constexpr int RW = 32 / CH;                        // keys a step
+    int pg[2];
+    pages(c, pg);
+    bool first = true;
+    int st = 0;
+    uint32_t ph = 1;
+    for (int64_t x = ps.x0; c.left > 0; ++x) {
+      const bool prefix = c.e < G;
+      const int wm = prefix ? WMP : WMO;
+      Blk d;
+      d.k1 = c.E.k1;
+      d.key = c.E.k0 + c.blk * kBN;
+      d.tok0 = c.E.tok0;
+      d.rows = c.E.rows;
+      d.tile = c.u / p.Hkv;
+      d.h = c.u - d.tile * p.Hkv;
+      d.unit = c.unit0 + c.u;
+      const AttnSet& set = prefix ? a.pre : a.own;
+      const bool stop = d.unit >= set.units;
+      const bool last = c.blk + 1 == c.nb || c.left == 1;
+      d.flags = (prefix ? BLK_PREFIX : 0) | (first ? BLK_FIRST : 0) |
+                (last ? BLK_LAST : 0) | (stop ? BLK_STOP : 0);
+      if (lane == 0 && c.blk == 0 && !stop) {
+        const int end = plan_owner(x + c.nb - 1, ps.total, ps.n);
+        set.meta[d.unit] =
+            make_int2(d.unit + (int)blockIdx.x, end - (int)blockIdx.x + 1);
+        if (c.u == 0) set.ebase[prefix ? c.e : c.e - G] = c.unit0 / p.Hkv;
+      }
+      // rows of the pool (32-bit numbers: 2^32 rows of 64 bytes are more
+      // than the memory)
+      uint32_t row[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = d.key + lane + 32 * i;
+        const bool ok = pg[i] >= 0 && pg[i] < p.num_pages;
+        if (!ok && pg[i] != -2) sv_latch(p.status, MPK_ERR_KV_PAGE);
+        row[i] = ok ? ((uint32_t)pg[i] * p.Hkv + d.h) * p.page_size +
+                          (t - (int)sv_div(t, p.page_div) * p.page_size)
+                    : 0xffffffffu;
+      }
+      // the next block's pages, on the way while this one waits for its stage
+      advance(c);
+      if (c.left > 0) pages(c, pg);
+      if (!bar_wait(empty + 8 * st, ph, dead)) break;
+      const uint32_t ks = t_addr(smem + st * C::kStage);
+      if (first && wm == 1 && !stop) {
+#pragma unroll
+        for (int i = 0; i < 16 / RW; ++i) {
+          const int r = r0 + i * RW, rw = d.tile * 16 + r;
+          const bool ok = rw < d.rows;
+          const int tok = ok ? rw / grp : 0;
+          cp16(ks + 2 * C::kTile + swz<D>(r, ch),
+               a.q + (d.tok0 + tok) * a.q_stride +
+                   (int64_t)(d.h * grp + (ok ? rw - tok * grp : 0)) * D +
+                   ch * 8,
+               ok ? 16 : 0);
+        }
+      }
+      const char* kp = reinterpret_cast<const char*>(p.k) + ch * 16;
+#pragma unroll
+      for (int i = 0; i < kBN / RW; ++i) {
+        const int r = r0 + i * RW;
+        const uint32_t rr =
+            __shfl_sync(0xffffffffu, row[i * RW / 32], r & 31);
+        const bool ok = rr != 0xffffffffu;
+        const char* src = kp + (uint64_t)(ok ? rr : 0u) * (D * 2);
+        const uint32_t dst = ks + swz<D>(r, ch);
+        cp16(dst, src, ok ? 16 : 0);
+        cp16(dst + C::kTile, src + dv, ok ? 16 : 0);
+      }
+      cp_arrive(full + 8 * st);
+      if (lane == 0) {
+        blk[st] = d;
+        bar_arrive(full + 8 * st);
+      }
+      if (stop) {   // q_start or group_start not ascending
+        sv_latch(p.status, MPK_ERR_INVALID_ARG);
+        break;
+      }
+      first = last;
+      if (++st == C::kStages) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+    cp_wait_all();
+  }
+};
+
+// What the blocks of a segment need to know.
+struct Seg {
+  int k1;              // end of the keys
+  int lim[2], lim_min; // keys this thread's two rows see
+  bool prefix;
+};
+
+// The warps that compute.
+template <int D>
+struct Attend {
+  using C = Cfg<D>;
+  static constexpr int CH = C::CH;
+
+  const AttendArgs& a;
+  uint8_t* smem;
+  float (*s_ml)[2];    // [4 * 16] of each warp's rows
+
+  uint32_t qf[D / 16][4];
+  float o[D / 8][4];
+  float m[2], l[2];
+
+  // This thread's part of the queries of the block's unit, in the layout of
+  // the product's first operand (rows past the entity's are zeros): from the
+  // stage, or for a larger tile from memory.
+  template <int WM>
+  __device__ __forceinline__ void queries(const Blk& b, int st) {
     const int lane = threadIdx.x & 31, wm = (threadIdx.x >> 5) % WM;
-    const int grp = p.Hq / p.Hkv, h = cu.u % p.Hkv, tile = cu.u / p.Hkv;
+    if constexpr (WM == 1) {
+      const uint32_t q = t_addr(smem + st * C::kStage + 2 * C::kTile);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        ldm4(q + swz<D>(lane & 15, 2 * k + (lane >> 4)), qf[k]);
+      return;
+    }
+    const PagedArgs& p = a.p;
+    const int grp = p.Hq / p.Hkv;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int row = tile * 16 * WM + wm * 16 + (lane >> 2) + 8 * r;
-      const bool ok = row < cu.E.rows;
+      const int row = b.tile * 16 * WM + wm * 16 + (lane >> 2) + 8 * r;
+      const bool ok = row < b.rows;
       const int tok = ok ? row / grp : 0;
-      const uint16_t* src = a.q + (cu.E.tok0 + tok) * a.q_stride +
-                            (int64_t)(h * grp + (ok ? row - tok * grp : 0)) * D +
+      const uint16_t* src = a.q + (b.tok0 + tok) * a.q_stride +
+                            (int64_t)(b.h * grp + (ok ? row - tok * grp : 0)) *
+                                D +
                             2 * (lane & 3);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        q[k][r] = ok ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k))
-                     : 0u;
-        q[k][2 + r] =
+        qf[k][r] = ok ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k))
+                      : 0u;
+        qf[k][2 + r] =
             ok ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 8))
                : 0u;
       }
@@ -212,17 +333,17 @@ struct Attend {
   }
 
   template <int WM>
-  __device__ __forceinline__ Seg begin(const Cursor& cu) {
+  __device__ __forceinline__ Seg begin(const Blk& b, int st) {
+    queries<WM>(b, st);
     Seg s;
-    s.k1 = cu.E.k1;
-    s.key = cu.E.k0 + cu.blk * kBN;
-    s.prefix = cu.e < G;
+    s.k1 = b.k1;
+    s.prefix = b.flags & BLK_PREFIX;
     if (s.prefix) {
       s.lim[0] = s.lim[1] = s.lim_min = s.k1;
     } else {
       // the last token's rows see all of k1; each token before one fewer
-      const int grp = a.p.Hq / a.p.Hkv, n = cu.E.rows / grp;
-      const int r0 = (cu.u / a.p.Hkv) * 16 * WM;
+      const int grp = a.p.Hq / a.p.Hkv, n = b.rows / grp;
+      const int r0 = b.tile * 16 * WM;
       const int lane = threadIdx.x & 31, wm = (threadIdx.x >> 5) % WM;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -238,13 +359,12 @@ struct Attend {
   }
 
   template <int WM>
-  __device__ __forceinline__ void block(const Seg& sg, int st) {
+  __device__ __forceinline__ void block(const Seg& sg, int kb, int st) {
     constexpr int WN = 4 / WM, NK = kBN / WN;   // keys a warp and block
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int wn = warp / WM;
     uint8_t* kt = smem + st * C::kStage;
     uint8_t* vt = kt + C::kTile;
-    const int kb = sg.key;
     // ---- scores
     float s[NK / 8][4];
 #pragma unroll
@@ -254,7 +374,7 @@ struct Attend {
 #pragma unroll
       for (int i = 0; i < NK / 16; ++i) {
         uint32_t b[4];
-        ldm4(s_addr(kt) + swz<D>(wn * NK + i * 16 + (lane & 7) +
+        ldm4(t_addr(kt) + swz<D>(wn * NK + i * 16 + (lane & 7) +
                                      ((lane >> 4) << 3),
                                  2 * k + ((lane >> 3) & 1)),
              b);
@@ -275,31 +395,38 @@ struct Attend {
       }
     }
     // ---- running maximum and sum
-    float mn[2] = {m[0], m[1]};
+    float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int i = 0; i < NK / 8; ++i) {
-      mn[0] = fmaxf(mn[0], fmaxf(s[i][0], s[i][1]));
-      mn[1] = fmaxf(mn[1], fmaxf(s[i][2], s[i][3]));
+      top[0] = fmaxf(top[0], fmaxf(s[i][0], s[i][1]));
+      top[1] = fmaxf(top[1], fmaxf(s[i][2], s[i][3]));
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      mn[r] = fmaxf(mn[r], __shfl_xor_sync(0xffffffffu, mn[r], 1));
-      mn[r] = fmaxf(mn[r], __shfl_xor_sync(0xffffffffu, mn[r], 2));
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
     }
-    float base[2];
+    // Weights are taken to a maximum that may lag behind by kSlack (their
+    // ratio cancels in o / l, and 2^kSlack is far from any limit), so few
+    // blocks rescale.
+    if (__any_sync(0xffffffffu,
+                   top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      // nothing seen yet: any finite base keeps every weight 0
-      base[r] = mn[r] == -INFINITY ? 0.f : mn[r];
-      const float f = ex2(m[r] - base[r]);
-      m[r] = mn[r];
-      l[r] *= f;
+      for (int r = 0; r < 2; ++r) {
+        const float mn = fmaxf(m[r], top[r]);
+        const float f = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
+        m[r] = mn;
+        l[r] *= f;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        o[i][2 * r] *= f;
-        o[i][2 * r + 1] *= f;
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][2 * r] *= f;
+          o[i][2 * r + 1] *= f;
+        }
       }
     }
+    // nothing seen yet: any finite base keeps every weight 0
+    const float base[2] = {m[0] == -INFINITY ? 0.f : m[0],
+                           m[1] == -INFINITY ? 0.f : m[1]};
     // Weights go to the product as bf16 (the type of V); the sum takes
     // them unrounded.  Each weight is off by at most 2^-8 of itself, and
     // independently, so the output's error stays about its own rounding.
@@ -319,14 +446,14 @@ struct Attend {
     // of the tile and added, key by key, to the rows that do see them.  (One
     // row per tile's limit: a block whose only limit is k1 has none.)
     if (masked && !sg.prefix && sg.lim_min < sg.k1)
-      fix_values<NK>(vt, kb, wn, sg.lim, pf);
+      fix_values<WM>(vt, kb, wn, sg.lim, pf);
     // ---- weighted values
 #pragma unroll
     for (int i = 0; i < NK / 16; ++i) {
 #pragma unroll
       for (int n = 0; n < D / 16; ++n) {
         uint32_t b[4];
-        ldm4t(s_addr(vt) + swz<D>(wn * NK + i * 16 + (lane & 15),
+        ldm4t(t_addr(vt) + swz<D>(wn * NK + i * 16 + (lane & 15),
                                   2 * n + (lane >> 4)),
               b);
         mma16816(o[2 * n], pf[i], b[0], b[1]);
@@ -371,7 +498,7 @@ struct Attend {
           s_ml[wn * M + row][0] = m[r];
           s_ml[wn * M + row][1] = l[r];
         }
-      __syncthreads();
+      sync_threads(1, kComp);
       float* buf = reinterpret_cast<float*>(smem + st * C::kStage);
       float f[2];
 #pragma unroll
@@ -397,7 +524,7 @@ struct Attend {
 #pragma unroll
       for (int r0 = 0; r0 < M; r0 += C::kPass) {
         if (r0 >= valid) break;
-        if (r0 > 0) __syncthreads();
+        if (r0 > 0) sync_threads(1, kComp);
 #pragma unroll
         for (int r = 0; r < 2; ++r)
           if (wm * 16 + 8 * r == r0) {
@@ -409,9 +536,9 @@ struct Attend {
                                          i * 8 + 2 * (lane & 3)) =
                   make_float2(o[i][2 * r] * f[r], o[i][2 * r + 1] * f[r]);
           }
-        __syncthreads();
+        sync_threads(1, kComp);
         const int n = min(valid - r0, C::kPass);
-        for (int i = tid; i < n * (D / 4); i += kNT) {
+        for (int i = tid; i < n * (D / 4); i += kComp) {
           const int row = i / (D / 4), c = i % (D / 4);
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -429,29 +556,33 @@ struct Attend {
     }
   }
 
-  template <int NK>
-  __device__ void fix_values(uint8_t* vt, int kb, int wn, const int (&lim)[2],
-                             const uint32_t (&pf)[NK / 16][4]) {
-    const int tid = threadIdx.x, lane = tid & 31;
-    if (tid < 2) s_bad[tid] = 0;
-    __syncthreads();
-    bool any = false;
-    for (int i = tid; i < kBN * CH; i += kNT) {
-      const int r = i / CH;
-      const uint4 u = *reinterpret_cast<const uint4*>(vt + swz<D>(r, i % CH));
+  // The 4 / WM slices of keys are private to the WM warps of a slice, which
+  // meet at a barrier of their own.
+  template <int WM>
+  __device__ __forceinline__ void fix_values(uint8_t* vt, int kb, int wn,
+                                          const int (&lim)[2],
+                                          const uint32_t (&pf)[4 * WM / 4][4]) {
+    constexpr int NK = 16 * WM;
+    const int lane = threadIdx.x & 31;
+    uint32_t bad[2] = {0, 0};    // keys of the slice with such a value
+    for (int i = lane; i < NK * CH; i += 32) {
+      const int k = i / CH;
+      const uint4 u =
+          *reinterpret_cast<const uint4*>(vt + swz<D>(wn * NK + k, i % CH));
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-      bool bad = false;
+      bool b = false;
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        bad |= (w[q] & 0x7f80u) == 0x7f80u ||
-               (w[q] & 0x7f800000u) == 0x7f800000u;
-      if (bad) atomicOr(&s_bad[r >> 5], 1u << (r & 31));
-      any |= bad;
+        b |= (w[q] & 0x7f80u) == 0x7f80u ||
+             (w[q] & 0x7f800000u) == 0x7f800000u;
+      if (b) bad[k >> 5] |= 1u << (k & 31);
     }
-    if (!__syncthreads_or(any)) return;
+    bad[0] = __reduce_or_sync(0xffffffffu, bad[0]);
+    bad[1] = __reduce_or_sync(0xffffffffu, bad[1]);
+    if (!(bad[0] | bad[1])) return;
     for (int k = 0; k < NK; ++k) {
       const int r = wn * NK + k;
-      if (!((s_bad[r >> 5] >> (r & 31)) & 1u)) continue;
+      if (!((bad[k >> 5] >> (k & 31)) & 1u)) continue;
       // the weights of key k: held by lane (k % 8) / 2 of each quad
       uint32_t w0 = 0, w1 = 0;
 #pragma unroll
@@ -476,9 +607,11 @@ struct Attend {
             o[i][q] += p[q >> 1] * v[q & 1];
       }
     }
-    __syncthreads();
-    for (int i = tid; i < kBN * CH; i += kNT) {
-      uint32_t* w = reinterpret_cast<uint32_t*>(vt + swz<D>(i / CH, i % CH));
+    if (WM > 1) sync_threads(2 + wn, 32 * WM);
+    else __syncwarp();
+    for (int i = lane; i < NK * CH; i += 32) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(
+          vt + swz<D>(wn * NK + i / CH, i % CH));
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t u = w[q];
@@ -487,103 +620,85 @@ struct Attend {
         w[q] = u;
       }
     }
-    __syncthreads();
+    if (WM > 1) sync_threads(2 + wn, 32 * WM);
+    else __syncwarp();
+  }
+
+  // The whole stretch of n blocks.
+  template <int WMP, int WMO>
+  __device__ __forceinline__ void run(const Blk* blk, uint32_t full,
+                                      uint32_t empty, volatile int* dead,
+                                      int64_t n) {
+    int st = 0;
+    uint32_t ph = 0;
+    Seg sg;
+    for (int64_t x = 0; x < n; ++x) {
+      if (!bar_wait(full + 8 * st, ph, dead)) return;
+      const Blk b = blk[st];
+      if (b.flags & BLK_STOP) return;
+      const bool prefix = b.flags & BLK_PREFIX;
+      const AttnSet& set = prefix ? a.pre : a.own;
+      const int64_t slot = (int64_t)b.unit + blockIdx.x;
+      if (WMP != WMO && prefix) {
+        if (b.flags & BLK_FIRST) sg = begin<WMP>(b, st);
+        block<WMP>(sg, b.key, st);
+        if (b.flags & BLK_LAST)
+          finish<WMP>(set, slot, b.rows - b.tile * 16 * WMP, st);
+      } else {
+        if (b.flags & BLK_FIRST) sg = begin<WMO>(b, st);
+        block<WMO>(sg, b.key, st);
+        if (b.flags & BLK_LAST)
+          finish<WMO>(set, slot, b.rows - b.tile * 16 * WMO, st);
+      }
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) bar_arrive(empty + 8 * st);
+      if (++st == C::kStages) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
   }
 };
 
 template <int D, int WMP, int WMO>
-__global__ void __launch_bounds__(kNT, 2)
+__global__ void __launch_bounds__(kNT, WMP > 1 ? 2 : Cfg<D>::kCtas)
     attend_kernel(const __grid_constant__ AttendArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int kStages = Cfg<D>::kStages;
   __shared__ float s_ml[64][2];
-  __shared__ uint32_t s_bad[2];
+  __shared__ Blk s_blk[kStages];
+  __shared__ __align__(8) uint64_t bars[2 * kStages];
+  __shared__ int s_dead;
+  const uint32_t full = t_addr(bars), empty = full + 8 * kStages;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      bar_init(full + 8 * i, 33);      // the copying lanes and one of them
+      bar_init(empty + 8 * i, 4);      // the computing warps
+    }
+    s_dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   // Behind the tensor-memory kernel (which has waited for everything before
   // it) nothing here depends on its results: start at once, and wait for it
   // at the end so that the merge, which waits for this kernel, has both.
   if (!a.tc) sv_grid_wait();
   sv_grid_launch();
-  using A = Attend<D, WMP, WMO>;
-  A t{a, smem, s_ml, s_bad, a.tc ? 0 : a.n_groups, 0};
-  t.n_ent = t.G + a.p.batch;
+  Copier<D, WMP, WMO> cp{a,     smem,    s_blk, full,
+                         empty, &s_dead, a.tc ? 0 : a.n_groups, 0};
+  cp.n_ent = cp.G + a.p.batch;
+  // (its barriers also publish the initialisation above)
   const PlanStart ps = plan_start<kNT, 16 * WMP, 16 * WMO, kBN>(
-      t.G, t.n_ent, a.p.Hkv, [&](int i) { return t.ent(i); }, blockIdx.x,
+      cp.G, cp.n_ent, a.p.Hkv, [&](int i) { return cp.ent(i); }, blockIdx.x,
       gridDim.x);
   if (ps.x0 < ps.x1) {
-    Cursor c;                    // the block being computed
-    c.e = ps.e;
-    c.unit0 = ps.unit0;
-    c.left = ps.x1 - ps.x0;
-    t.enter(c);
-    c.u = (int)(ps.off / c.nb);
-    c.blk = (int)(ps.off - (int64_t)c.u * c.nb);
-    Cursor f = c;                // the block to be copied next
-    for (int s = 0; s < kStages - 1; ++s) {
-      if (f.left > 0) {
-        t.load(f, s);
-        t.advance(f);
-      }
-      cp_commit();
+    if (threadIdx.x >= kComp) {
+      cp.run(ps);
+    } else {
+      Attend<D> t{a, smem, s_ml};
+      t.template run<WMP, WMO>(s_blk, full, empty, &s_dead, ps.x1 - ps.x0);
     }
-    if (c.e < t.G) t.template queries<WMP>(c, t.qf);
-    else t.template queries<WMO>(c, t.qf);
-    int64_t x = ps.x0;
-    int st = 0;
-    bool fresh = true;
-    Seg sg;
-    while (c.left > 0) {
-      cp_wait<kStages - 2>();
-      __syncthreads();
-      if (f.left > 0) {
-        t.load(f, st == 0 ? kStages - 1 : st - 1);
-        t.advance(f);
-      }
-      cp_commit();
-      const bool prefix = c.e < t.G;
-      if (fresh) {
-        sg = prefix ? t.template begin<WMP>(c) : t.template begin<WMO>(c);
-        const AttnSet& set = prefix ? a.pre : a.own;
-        if (c.unit0 + c.u >= set.units) {
-          // q_start or group_start not ascending
-          sv_latch(a.p.status, MPK_ERR_INVALID_ARG);
-          break;
-        }
-        if (c.blk == 0 && threadIdx.x == 0) {
-          const int last = plan_owner(x + c.nb - 1, ps.total, ps.n);
-          set.meta[c.unit0 + c.u] = make_int2(
-              c.unit0 + c.u + (int)blockIdx.x, last - (int)blockIdx.x + 1);
-          if (c.u == 0) set.ebase[prefix ? c.e : c.e - t.G] = c.unit0 / a.p.Hkv;
-        }
-      }
-      const int64_t slot = (int64_t)c.unit0 + c.u + blockIdx.x;
-      const int tile = c.u / a.p.Hkv, rows = c.E.rows;
-      const bool last = c.blk + 1 == c.nb || c.left == 1;
-      t.advance(c);
-      uint32_t qn[D / 16][4];
-      if (last && c.left > 0) {
-        if (c.e < t.G) t.template queries<WMP>(c, qn);
-        else t.template queries<WMO>(c, qn);
-      }
-      if (prefix) {
-        t.template block<WMP>(sg, st);
-        if (last)
-          t.template finish<WMP>(a.pre, slot, rows - tile * 16 * WMP, st);
-      } else {
-        t.template block<WMO>(sg, st);
-        if (last)
-          t.template finish<WMO>(a.own, slot, rows - tile * 16 * WMO, st);
-      }
-      if (last) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) t.qf[k][i] = qn[k][i];
-      }
-      fresh = last;
-      sg.key += kBN;
-      ++x;
-      st = st + 1 == kStages ? 0 : st + 1;
-    }
-    cp_wait<0>();
+    __syncthreads();
+    if (threadIdx.x == 0 && s_dead) sv_latch(a.p.status, MPK_ERR_TIMEOUT);
   }
   if (a.tc) sv_grid_wait();
 }
@@ -594,7 +709,8 @@ cudaError_t run_tiles(const AttendArgs& a, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(
       k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return sv_launch(k, dim3(attend_ctas()), kNT, Cfg<D>::kSmem, s, true, a);
+  const int ctas = WMP > 1 ? 2 : Cfg<D>::kCtas;
+  return sv_launch(k, dim3(attend_ctas() / 4 * ctas), kNT, Cfg<D>::kSmem, s, true, a);
 }
 
 template <int D>

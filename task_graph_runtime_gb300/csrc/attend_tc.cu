@@ -34,59 +34,9 @@ constexpr int kSoftRegs = 216, kOtherRegs = 72;
 constexpr int kRows = 256;        // rows of a tile
 constexpr int kKeys = 128;        // keys of a block
 constexpr float kSlack = 8.f;
-constexpr uint64_t kWaitNs = 2000000000ull;    // longest wait of a role
-constexpr uint64_t kDrainNs = 200000000ull;    // and for copies at the end
+constexpr uint64_t kDrainNs = 200000000ull;    // longest wait for copies at
+                                               // the end
 
-__device__ __forceinline__ uint32_t t_addr(const void* p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
-__device__ __forceinline__ void bar_init(uint32_t b, uint32_t n) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint32_t b) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(b) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint32_t b, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
-                   b),
-               "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ bool bar_try(uint32_t b, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(b), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// Waits for a phase, for two seconds at most; after that (or when another
-// role has given up) false, and every role leaves its loop.
-__device__ __forceinline__ bool bar_wait(uint32_t b, uint32_t parity,
-                                         volatile int* dead,
-                                         uint64_t limit = kWaitNs) {
-  bool ok = bar_try(b, parity);
-  if (!ok) {
-    uint64_t t0, t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-    for (uint32_t i = 1; !ok; ++i) {
-      ok = bar_try(b, parity);
-      if (!ok && (i & 63u) == 0u) {
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-        if (*dead || t - t0 > limit) {
-          *dead = 1;
-          break;
-        }
-      }
-    }
-  }
-  // a warp goes on, or leaves, as one
-  return __all_sync(0xffffffffu, ok);
-}
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map,
                                        int x, int y, uint32_t bar) {
   asm volatile(
