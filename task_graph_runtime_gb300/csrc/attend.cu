@@ -130,6 +130,43 @@ __global__ void __launch_bounds__(kNT)
                            0.69314718055994530942);
 }
 
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
+                             void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*,
+                             CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The layer's pool as rows of d values, in boxes of `box` rows x 128 bytes (the
+// whole row of 64 for 32 values), swizzled as the kernels read them.
+bool page_map(EncodeFn fn, const PagedArgs& p, const void* pool, int box,
+              CUtensorMap* m) {
+  const cuuint64_t dims[2] = {
+      (cuuint64_t)p.d, (cuuint64_t)p.num_pages * p.Hkv * p.page_size};
+  const cuuint64_t strides[1] = {(cuuint64_t)p.d * 2};
+  const cuuint32_t boxes[2] = {p.d < 64 ? 32u : 64u, (cuuint32_t)box};
+  const cuuint32_t steps[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool),
+            dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            p.d < 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool page_maps(AttendArgs* a) {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                         cudaEnableDefault, &r) !=
+            cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn && page_map(fn, a->p, a->p.k, a->box, &a->map_k) &&
+         page_map(fn, a->p, a->p.v, a->box, &a->map_v);
+}
+
 template <int D>
 cudaError_t run_merge(const AttendArgs& a, cudaStream_t s) {
   const int64_t warps = (int64_t)a.p.n_tokens * a.p.Hq;
@@ -142,6 +179,15 @@ cudaError_t run_merge(const AttendArgs& a, cudaStream_t s) {
 
 // at most: one CTA for each of four places on 152 SMs
 int attend_ctas() { return 152 * 4; }
+
+// Keys of a page that one TMA box takes: a power of two (so that a block of
+// keys is whole boxes) that divides the page; 0, and no TMA, when that is
+// below the 8 rows of a swizzle group or the pool's rows pass a coordinate.
+int attend_box(const PagedArgs& p) {
+  if ((int64_t)p.num_pages * p.Hkv * p.page_size > 0x7fffffff) return 0;
+  const int box = p.page_size & -p.page_size;
+  return box < 8 ? 0 : box > 64 ? 64 : box;
+}
 
 // Chooses the launches and places their results.
 size_t attend_workspace(AttendArgs* a, char* base) {
@@ -157,7 +203,8 @@ size_t attend_workspace(AttendArgs* a, char* base) {
   const int64_t all = a->n_groups ? (rows + a->n_groups - 1) / a->n_groups : 0;
   // the smallest row tiles that hold them; few pairs are built
   a->wmo = per <= 16 ? 1 : per <= 32 ? 2 : 4;
-  a->tc = all > 64 && attend_tc_box(a->p) && a->scale_log2 > 0.f;
+  a->box = attend_box(a->p);
+  a->tc = all > 64 && a->box && a->p.d >= 64 && a->scale_log2 > 0.f;
   a->wmp = a->wmo > 1 || (all > 16 && !a->tc) ? 4 : 1;
   a->own.M = 16 * a->wmo;
   a->pre.M = a->tc ? attend_tc_rows() : 16 * a->wmp;
@@ -177,7 +224,8 @@ size_t attend_workspace(AttendArgs* a, char* base) {
   return off;
 }
 
-cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
+cudaError_t launch_attend(AttendArgs& a, cudaStream_t s) {
+  if (a.box && !page_maps(&a)) return cudaErrorNotSupported;
   cudaError_t e = cudaSuccess;
   if (a.tc) e = launch_attend_tc(a, s);
   if (e != cudaSuccess) return e;

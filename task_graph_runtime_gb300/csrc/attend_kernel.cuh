@@ -15,11 +15,12 @@
 // of 64; mma.sync m16n8k16, scores and weights stay in registers.  With few
 // rows the warps split the keys, so that the tensor instructions per block
 // stay few; the kernel is bound by the K/V bytes.
-// A fifth warp walks the stretch ahead of them: it looks up the pages (any
-// page size, one block early), copies K, V and the queries of a 16-row tile
-// into a ring of kStages shared-memory stages (16-byte asynchronous copies
-// that arrive on the stage's barrier), and leaves a description of the block
-// there.  The others touch no list, table or length, and a stretch of many
+// A fifth warp walks the stretch ahead of them: it looks up the pages (one
+// block early), copies K, V and the queries of a 16-row tile into a ring of
+// kStages shared-memory stages, and leaves a description of the block there.
+// Pages that are a multiple of 8 tokens come as TMA boxes, others key by key
+// in 16-byte copies (one warp's 64 such instructions a block took longer than
+// the block: 66 us instead of CHECK at 256 sequences of 1..512 own keys).  The others touch no list, table or length, and a stretch of many
 // short sequences streams like one long one: the chain lengths -> pages ->
 // keys that starts a sequence runs while earlier blocks are computed.
 #pragma once
@@ -31,6 +32,7 @@ namespace {
 
 constexpr int kNT = 160;       // four warps that compute, one that copies
 constexpr int kComp = 128;
+constexpr uint64_t kDrainNs = 200000000ull;   // for copies at the end
 constexpr int kBN = 64;
 constexpr float kSlack = 8.f;
 
@@ -82,15 +84,18 @@ __device__ __forceinline__ float ex2(float x) {
 // Byte offset of 16-byte chunk c of row r in a tile of D-value rows.  The
 // chunk index is mixed with the row so that the 8 rows an ldmatrix reads lie
 // in different banks.
-template <int D>
+// (rows of 128 values: two panels of 64).  These are the 64- and 128-byte
+// swizzles of TMA.
+template <int D, int ROWS>
 __device__ __forceinline__ uint32_t swz(int r, int c) {
   if (D == 32) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-  return r * (D * 2) + ((c ^ (r & 7)) << 4);
+  return (c >> 3) * (ROWS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
 // What the copying warp says of the block in a stage.
 struct Blk {
-  int k1, key;         // end of the unit's keys, first key of the block
+  int k0, k1;          // the unit's keys
+  int key;             // first key of the block (a multiple of kBN)
   int tok0, rows;      // its entity's first token row and rows
   int tile, h;         // row tile, KV head
   int unit;
@@ -106,8 +111,9 @@ struct Cfg {
   static constexpr int kStages = D == 128 ? 3 : 4;
   static constexpr int kTile = kBN * D * 2;            // bytes of K (or V)
   static constexpr int kQ = 16 * D * 2;                // queries of 16 rows
-  static constexpr int kStage = 2 * kTile + kQ;
-  static constexpr int kSmem = kStages * kStage;
+  // (stages on 1024 bytes: the period of the swizzle)
+  static constexpr int kStage = (2 * kTile + kQ + 1023) / 1024 * 1024;
+  static constexpr int kSmem = kStages * kStage + 1024;
   static constexpr int CH = D / 8;                     // chunks a row
   static constexpr int kPitch = D + 4;                 // merge buffer, floats
   // rows that the merge of four key slices takes at a time (it lies over a
@@ -141,7 +147,7 @@ struct Copier {
   __device__ __forceinline__ void enter(Cursor& c) const {
     const int M = c.e < G ? 16 * WMP : 16 * WMO;
     c.E = ent(c.e);
-    c.nb = (c.E.k1 - c.E.k0 + kBN - 1) / kBN;
+    c.nb = blocks_of<kBN>(c.E);
     c.units = c.nb > 0 ? ((c.E.rows + M - 1) / M) * a.p.Hkv : 0;
   }
   __device__ __forceinline__ void advance(Cursor& c) const {
@@ -161,15 +167,22 @@ struct Copier {
     } while (c.units == 0);
     c.u = 0;
   }
-  // Lane i looks up the pages of keys i and i + 32 of the cursor's block; -2
-  // for keys past the end.
+  __device__ __forceinline__ int first_key(const Cursor& c) const {
+    return (c.E.k0 / kBN + c.blk) * kBN;
+  }
+  // Lane i looks up the pages of keys (boxes) i and i + 32 of the cursor's
+  // block; -2 for those outside the entity's keys.
   __device__ __forceinline__ void pages(const Cursor& c, int (&pg)[2]) const {
     const int lane = threadIdx.x & 31;
     const int32_t* pt = a.p.page_table + (int64_t)c.E.seq * a.p.max_pages;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int t = c.E.k0 + c.blk * kBN + lane + 32 * i;
-      pg[i] = t < c.E.k1 ? __ldg(pt + sv_div(t, a.p.page_div)) : -2;
+      // with TMA, one lane a box
+      const int t = first_key(c) + (lane + 32 * i) * (a.box ? a.box : 1);
+      const int n = a.box ? a.box : 1;
+      pg[i] = t + n > c.E.k0 && t < c.E.k1 && (lane + 32 * i) * n < kBN
+                  ? __ldg(pt + sv_div(t, a.p.page_div))
+                  : -2;
     }
   }
 
@@ -197,8 +210,9 @@ struct Copier {
       const bool prefix = c.e < G;
       const int wm = prefix ? WMP : WMO;
       Blk d;
+      d.k0 = c.E.k0;
       d.k1 = c.E.k1;
-      d.key = c.E.k0 + c.blk * kBN;
+      d.key = first_key(c);
       d.tok0 = c.E.tok0;
       d.rows = c.E.rows;
       d.tile = c.u / p.Hkv;
@@ -220,7 +234,7 @@ struct Copier {
       uint32_t row[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int t = d.key + lane + 32 * i;
+        const int t = d.key + (lane + 32 * i) * (a.box ? a.box : 1);
         const bool ok = pg[i] >= 0 && pg[i] < p.num_pages;
         if (!ok && pg[i] != -2) sv_latch(p.status, MPK_ERR_KV_PAGE);
         row[i] = ok ? ((uint32_t)pg[i] * p.Hkv + d.h) * p.page_size +
@@ -238,29 +252,53 @@ struct Copier {
           const int r = r0 + i * RW, rw = d.tile * 16 + r;
           const bool ok = rw < d.rows;
           const int tok = ok ? rw / grp : 0;
-          cp16(ks + 2 * C::kTile + swz<D>(r, ch),
+          cp16(ks + 2 * C::kTile + swz<D, 16>(r, ch),
                a.q + (d.tok0 + tok) * a.q_stride +
                    (int64_t)(d.h * grp + (ok ? rw - tok * grp : 0)) * D +
                    ch * 8,
                ok ? 16 : 0);
         }
       }
-      const char* kp = reinterpret_cast<const char*>(p.k) + ch * 16;
+      uint32_t bytes = 0;
+      if (a.box) {
+        const bool ok = row[0] != 0xffffffffu;
+        bytes = __popc(__ballot_sync(0xffffffffu, ok)) * a.box * D * 4;
+        // (the bytes are announced first)
+        if (lane == 0) {
+          blk[st] = d;
+          bar_expect(full + 8 * st, bytes);
+        }
+        __syncwarp();
+        if (ok) {
+          const uint32_t dst = ks + lane * a.box * (D < 64 ? 64 : 128);
 #pragma unroll
-      for (int i = 0; i < kBN / RW; ++i) {
-        const int r = r0 + i * RW;
-        const uint32_t rr =
-            __shfl_sync(0xffffffffu, row[i * RW / 32], r & 31);
-        const bool ok = rr != 0xffffffffu;
-        const char* src = kp + (uint64_t)(ok ? rr : 0u) * (D * 2);
-        const uint32_t dst = ks + swz<D>(r, ch);
-        cp16(dst, src, ok ? 16 : 0);
-        cp16(dst + C::kTile, src + dv, ok ? 16 : 0);
-      }
-      cp_arrive(full + 8 * st);
-      if (lane == 0) {
-        blk[st] = d;
-        bar_arrive(full + 8 * st);
+          for (int q = 0; q < (D + 63) / 64; ++q) {
+            tma_2d(dst + q * kBN * 128, &a.map_k, 64 * q, (int)row[0],
+                   full + 8 * st);
+            tma_2d(dst + C::kTile + q * kBN * 128, &a.map_v, 64 * q,
+                   (int)row[0], full + 8 * st);
+          }
+        }
+        cp_arrive(full + 8 * st);
+      } else {
+        const char* kp = reinterpret_cast<const char*>(p.k) + ch * 16;
+#pragma unroll 4
+        for (int i = 0; i < kBN / RW; ++i) {
+          const int r = r0 + i * RW;
+          const uint32_t lo = __shfl_sync(0xffffffffu, row[0], r & 31);
+          const uint32_t hi = __shfl_sync(0xffffffffu, row[1], r & 31);
+          const uint32_t rr = r < 32 ? lo : hi;
+          const bool ok = rr != 0xffffffffu;
+          const char* src = kp + (uint64_t)(ok ? rr : 0u) * (D * 2);
+          const uint32_t dst = ks + swz<D, kBN>(r, ch);
+          cp16(dst, src, ok ? 16 : 0);
+          cp16(dst + C::kTile, src + dv, ok ? 16 : 0);
+        }
+        cp_arrive(full + 8 * st);
+        if (lane == 0) {
+          blk[st] = d;
+          bar_arrive(full + 8 * st);
+        }
       }
       if (stop) {   // q_start or group_start not ascending
         sv_latch(p.status, MPK_ERR_INVALID_ARG);
@@ -273,13 +311,20 @@ struct Copier {
       }
     }
     cp_wait_all();
+    // no box may land after the CTA has left
+    int late = 0;
+    const int64_t sent = ps.x1 - ps.x0 - c.left;
+    for (int64_t i = sent < C::kStages ? 0 : sent - C::kStages;
+         a.box && i < sent; ++i)
+      bar_wait(full + 8 * (int)(i % C::kStages),
+               (uint32_t)(i / C::kStages) & 1u, &late, kDrainNs);
   }
 };
 
 // What the blocks of a segment need to know.
 struct Seg {
-  int k1;              // end of the keys
-  int lim[2], lim_min; // keys this thread's two rows see
+  int k0, k1;          // the keys
+  int lim[2], lim_min; // keys this thread's two rows see: [k0, lim)
   bool prefix;
 };
 
@@ -307,7 +352,7 @@ struct Attend {
       const uint32_t q = t_addr(smem + st * C::kStage + 2 * C::kTile);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
-        ldm4(q + swz<D>(lane & 15, 2 * k + (lane >> 4)), qf[k]);
+        ldm4(q + swz<D, 16>(lane & 15, 2 * k + (lane >> 4)), qf[k]);
       return;
     }
     const PagedArgs& p = a.p;
@@ -336,6 +381,7 @@ struct Attend {
   __device__ __forceinline__ Seg begin(const Blk& b, int st) {
     queries<WM>(b, st);
     Seg s;
+    s.k0 = b.k0;
     s.k1 = b.k1;
     s.prefix = b.flags & BLK_PREFIX;
     if (s.prefix) {
@@ -374,7 +420,7 @@ struct Attend {
 #pragma unroll
       for (int i = 0; i < NK / 16; ++i) {
         uint32_t b[4];
-        ldm4(t_addr(kt) + swz<D>(wn * NK + i * 16 + (lane & 7) +
+        ldm4(t_addr(kt) + swz<D, kBN>(wn * NK + i * 16 + (lane & 7) +
                                      ((lane >> 4) << 3),
                                  2 * k + ((lane >> 3) & 1)),
              b);
@@ -382,7 +428,7 @@ struct Attend {
         mma16816(s[2 * i + 1], qf[k], b[2], b[3]);
       }
     }
-    const bool masked = kb + kBN > sg.lim_min;
+    const bool masked = kb + kBN > sg.lim_min || kb < sg.k0;
 #pragma unroll
     for (int i = 0; i < NK / 8; ++i) {
 #pragma unroll
@@ -391,7 +437,8 @@ struct Attend {
         const int key = kb + wn * NK + i * 8 + 2 * (lane & 3);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (key + (q & 1) >= sg.lim[q >> 1]) s[i][q] = -INFINITY;
+          if (key + (q & 1) >= sg.lim[q >> 1] || key + (q & 1) < sg.k0)
+            s[i][q] = -INFINITY;
       }
     }
     // ---- running maximum and sum
@@ -441,10 +488,12 @@ struct Attend {
       pf[i / 2][(i & 1) * 2 + 1] = sv_pack(p2, p3);
     }
     // A weight of 0 times an infinite or NaN value of V would spoil a row
-    // that does not see that key.  Keys past k1 are zeros; in a block that
-    // some rows see only in part, values that are not finite are taken out
-    // of the tile and added, key by key, to the rows that do see them.  (One
-    // row per tile's limit: a block whose only limit is k1 has none.)
+    // that does not see that key.  Values of keys outside [k0, k1) become
+    // zeros; in a block that some rows see only in part, values that are not
+    // finite are taken out of the tile and added, key by key, to the rows
+    // that do see them.
+    if (a.box && (kb < sg.k0 || kb + kBN > sg.k1))
+      clear_values<WM>(vt, sg.k0 - kb, sg.k1 - kb, wn);
     if (masked && !sg.prefix && sg.lim_min < sg.k1)
       fix_values<WM>(vt, kb, wn, sg.lim, pf);
     // ---- weighted values
@@ -453,7 +502,7 @@ struct Attend {
 #pragma unroll
       for (int n = 0; n < D / 16; ++n) {
         uint32_t b[4];
-        ldm4t(t_addr(vt) + swz<D>(wn * NK + i * 16 + (lane & 15),
+        ldm4t(t_addr(vt) + swz<D, kBN>(wn * NK + i * 16 + (lane & 15),
                                   2 * n + (lane >> 4)),
               b);
         mma16816(o[2 * n], pf[i], b[0], b[1]);
@@ -553,7 +602,25 @@ struct Attend {
           *reinterpret_cast<float4*>(part + (r0 + row) * D + c * 4) = v;
         }
       }
+      fence_async();   // the buffer, before a box lands on it
     }
+  }
+
+  // Zeros for the keys of this warp's slice outside [lo, hi).
+  template <int WM>
+  __device__ __forceinline__ void clear_values(uint8_t* vt, int lo, int hi,
+                                               int wn) {
+    constexpr int NK = 16 * WM;
+    const int lane = threadIdx.x & 31, wm = (threadIdx.x >> 5) % WM;
+    for (int i = wm * 32 + lane; i < NK * CH; i += 32 * WM) {
+      const int r = wn * NK + i / CH;
+      if (r < lo || r >= hi)
+        *reinterpret_cast<uint4*>(vt + swz<D, kBN>(r, i % CH)) =
+            make_uint4(0, 0, 0, 0);
+    }
+    if (WM > 1) sync_threads(2 + wn, 32 * WM);
+    else __syncwarp();
+    fence_async();     // before a box lands here again
   }
 
   // The 4 / WM slices of keys are private to the WM warps of a slice, which
@@ -568,7 +635,7 @@ struct Attend {
     for (int i = lane; i < NK * CH; i += 32) {
       const int k = i / CH;
       const uint4 u =
-          *reinterpret_cast<const uint4*>(vt + swz<D>(wn * NK + k, i % CH));
+          *reinterpret_cast<const uint4*>(vt + swz<D, kBN>(wn * NK + k, i % CH));
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
       bool b = false;
 #pragma unroll
@@ -599,7 +666,7 @@ struct Attend {
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         const uint32_t u = *reinterpret_cast<const uint32_t*>(
-            vt + swz<D>(r, i) + 4 * (lane & 3));
+            vt + swz<D, kBN>(r, i) + 4 * (lane & 3));
         const float v[2] = {sv_lo(u), sv_hi(u)};
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -611,7 +678,7 @@ struct Attend {
     else __syncwarp();
     for (int i = lane; i < NK * CH; i += 32) {
       uint32_t* w = reinterpret_cast<uint32_t*>(
-          vt + swz<D>(wn * NK + i / CH, i % CH));
+          vt + swz<D, kBN>(wn * NK + i / CH, i % CH));
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t u = w[q];
@@ -622,6 +689,7 @@ struct Attend {
     }
     if (WM > 1) sync_threads(2 + wn, 32 * WM);
     else __syncwarp();
+    fence_async();
   }
 
   // The whole stretch of n blocks.
@@ -663,7 +731,8 @@ struct Attend {
 template <int D, int WMP, int WMO>
 __global__ void __launch_bounds__(kNT, WMP > 1 ? 2 : Cfg<D>::kCtas)
     attend_kernel(const __grid_constant__ AttendArgs a) {
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t raw[];
+  uint8_t* const smem = raw + (1024 - (t_addr(raw) & 1023)) % 1024;
   constexpr int kStages = Cfg<D>::kStages;
   __shared__ float s_ml[64][2];
   __shared__ Blk s_blk[kStages];

@@ -73,6 +73,17 @@ __device__ __forceinline__ bool bar_wait(uint32_t b, uint32_t parity,
   // a warp goes on, or leaves, as one
   return __all_sync(0xffffffffu, ok);
 }
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map,
+                                       int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
 
 // ---- the plan
 struct Ent {
@@ -136,6 +147,12 @@ __device__ __forceinline__ Ent att_seq_ent(const AttendArgs& a, int b) {
   return e;
 }
 
+// Blocks of an entity's keys; they begin at multiples of BN.
+template <int BN>
+__device__ __forceinline__ int blocks_of(const Ent& e) {
+  return e.k1 > e.k0 ? (e.k1 + BN - 1) / BN - e.k0 / BN : 0;
+}
+
 // Where a CTA starts on the line.
 struct PlanStart {
   int64_t x0, x1;      // this CTA's stretch
@@ -160,7 +177,7 @@ __device__ __forceinline__ PlanStart plan_start(int G, int n_ent, int Hkv,
     cost = unit = 0;
     if (i < n_ent) {
       const Ent e = ent(i);
-      const int64_t nb = (e.k1 - e.k0 + BN - 1) / BN;
+      const int64_t nb = blocks_of<BN>(e);
       const int64_t nt =
           i < G ? (e.rows + MP - 1) / MP : (e.rows + MO - 1) / MO;
       cost = nb * nt * Hkv;

@@ -19,8 +19,6 @@
 // has grown by more than 2^kSlack over the one its weights are taken to
 // (their ratio cancels in O / l; 2^8 is far from any limit of fp32 or bf16), so
 // nearly every block leaves it alone.
-#include <cuda.h>
-
 #include "attend_plan.cuh"
 
 namespace mpk {
@@ -37,17 +35,6 @@ constexpr float kSlack = 8.f;
 constexpr uint64_t kDrainNs = 200000000ull;    // longest wait for copies at
                                                // the end
 
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map,
-                                       int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void fence_async() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
 __device__ __forceinline__ void tc_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
@@ -150,9 +137,7 @@ struct TcSmem {
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsT, 1)
-    attend_tc(const __grid_constant__ AttendArgs a,
-              const __grid_constant__ CUtensorMap mk,
-              const __grid_constant__ CUtensorMap mv, int box) {
+    attend_tc(const __grid_constant__ AttendArgs a) {
   using L = TcSmem<D>;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t bars[20];
@@ -198,6 +183,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   // everything before this kernel is complete: the next one may start
   sv_grid_launch();
   const PagedArgs& p = a.p;
+  const int box = a.box;
   const int Hkv = p.Hkv, grp = p.Hq / p.Hkv;
   const PlanStart st = plan_start<kThreadsT, kRows, kRows, kKeys>(
       a.n_groups, a.n_groups, Hkv, [&](int g) { return att_group_ent(a, g); }, blockIdx.x,
@@ -280,7 +266,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           if (row >= 0)
 #pragma unroll
             for (int q = 0; q < L::kPanels; ++q)
-              tma_2d(dst + q * L::kPanel + lane * box * 128, kv ? &mv : &mk,
+              tma_2d(dst + q * L::kPanel + lane * box * 128, kv ? &a.map_v : &a.map_k,
                      q * 64, row, bar);
           if (fill) {
             // values of keys past the end: zeros, because a weight of 0
@@ -520,35 +506,14 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   }
 }
 
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
-                             void*, const cuuint64_t*, const cuuint64_t*,
-                             const cuuint32_t*, const cuuint32_t*,
-                             CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// Pages as rows of d values, in boxes of `box` rows x 64 values.
-bool page_map(EncodeFn fn, const PagedArgs& p, const void* pool, int box,
-              CUtensorMap* m) {
-  const cuuint64_t dims[2] = {
-      (cuuint64_t)p.d, (cuuint64_t)p.num_pages * p.Hkv * p.page_size};
-  const cuuint64_t strides[1] = {(cuuint64_t)p.d * 2};
-  const cuuint32_t boxes[2] = {64, (cuuint32_t)box};
-  const cuuint32_t steps[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool),
-            dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D>
-cudaError_t tc_d(const AttendArgs& a, const CUtensorMap& mk,
-                 const CUtensorMap& mv, int box, cudaStream_t s) {
+cudaError_t tc_d(const AttendArgs& a, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(
       attend_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
       TcSmem<D>::kSmem);
   if (e != cudaSuccess) return e;
   return sv_launch(attend_tc<D>, dim3(attend_tc_ctas()), kThreadsT,
-                   TcSmem<D>::kSmem, s, true, a, mk, mv, box);
+                   TcSmem<D>::kSmem, s, true, a);
 }
 
 }  // namespace
@@ -556,35 +521,8 @@ cudaError_t tc_d(const AttendArgs& a, const CUtensorMap& mk,
 int attend_tc_ctas() { return 152; }
 int attend_tc_rows() { return kRows; }
 
-// Rows of a page that one TMA box takes: a power of two (so that blocks of
-// 128 keys are whole boxes) that divides the page; 0 when that is below the 8
-// rows of a swizzle group, or the head or the pool does not fit.
-int attend_tc_box(const PagedArgs& p) {
-  if (p.d != 64 && p.d != 128) return 0;
-  if ((int64_t)p.num_pages * p.Hkv * p.page_size > 0x7fffffff) return 0;
-  int box = p.page_size & -p.page_size;
-  if (box > 128) box = 128;
-  return box < 8 ? 0 : box;
-}
-
 cudaError_t launch_attend_tc(const AttendArgs& a, cudaStream_t s) {
-  static const EncodeFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                         cudaEnableDefault, &r) !=
-            cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeFn>(p);
-  }();
-  const int box = attend_tc_box(a.p);
-  CUtensorMap mk, mv;
-  if (!fn || !box || !page_map(fn, a.p, a.p.k, box, &mk) ||
-      !page_map(fn, a.p, a.p.v, box, &mv))
-    return cudaErrorNotSupported;
-  return a.p.d == 128 ? tc_d<128>(a, mk, mv, box, s)
-                      : tc_d<64>(a, mk, mv, box, s);
+  return a.p.d == 128 ? tc_d<128>(a, s) : tc_d<64>(a, s);
 }
 
 }  // namespace mpk

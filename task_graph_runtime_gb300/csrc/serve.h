@@ -3,6 +3,7 @@
 // sequence, shared prefixes, drafted tokens.  The C ABI is in serve_api.cpp.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -80,6 +81,8 @@ struct AttendArgs {
   AttnSet own, pre;            // results of the sequences, of the groups
   int tc;                      // prefixes by the tensor-memory kernel
   int wmp, wmo;                // row tiles of attend_kernel (16 x these)
+  int box;                     // keys a TMA box takes; 0: no TMA
+  CUtensorMap map_k, map_v;       // the layer's pools, if box > 0
 };
 int attend_ctas();
 // the general kernel, one translation unit per head_dim
@@ -88,11 +91,11 @@ cudaError_t launch_attend_64(const AttendArgs& a, cudaStream_t s);
 cudaError_t launch_attend_128(const AttendArgs& a, cudaStream_t s);
 int attend_tc_ctas();
 int attend_tc_rows();
-int attend_tc_box(const PagedArgs& p);
+int attend_box(const PagedArgs& p);
 cudaError_t launch_attend_tc(const AttendArgs& a, cudaStream_t s);
 // Workspace bytes, and the pointers of *a into it (base may be null).
 size_t attend_workspace(AttendArgs* a, char* base);
-cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s);
+cudaError_t launch_attend(AttendArgs& a, cudaStream_t s);
 
 struct VerifyArgs {
   int batch, n_tokens, vocab, max_out;
