@@ -1,13 +1,15 @@
 // Appending new tokens to the paged KV cache (mpk_kv_append) and the
 // rotation table it reads (mpk_rope_table).
 //
-// One thread takes 16 values of one head of one token: two 16-byte chunks
-// that hold both members of 8 rotation pairs (half layout: chunk i and the
-// chunk rot/2 values later; interleaved: two neighbouring chunks), so that a
-// rotation needs no exchange between threads.  A head's d/16 threads sit in
-// one warp and sum its squares with log2(d/16) shuffles.  A thread repeats
-// this for up to kHeads heads of its token with the same cosines and sines in
-// registers: the table row is read once per kHeads heads.
+// One thread takes 16 values of a head: two 16-byte chunks that hold both
+// members of 8 rotation pairs (half layout: chunk i and the chunk rot/2 values
+// later; interleaved: two neighbouring chunks), so that a rotation needs no
+// exchange between threads.  A head's d/16 threads sit in one warp and sum its
+// squares with log2(d/16) shuffles.  A thread stays with its token and its
+// place in the head and goes over every HS-th head, so the cosines and sines
+// (and what the token's position leads to) are found once, and the next two
+// heads are on the way while two are worked on.  Arithmetic is on pairs of
+// fp32 values (twice the rate), each operation rounded as by itself.
 //
 // Bound by HBM: every input and output byte moves once.
 #include "serve_dev.cuh"
@@ -15,67 +17,68 @@
 namespace mpk {
 namespace {
 
-constexpr int kThreadsA = 128;
+constexpr int kThreadsA = 256;
 
-__device__ __forceinline__ void unpack8(uint4 u, float* x) {
-  x[0] = sv_lo(u.x); x[1] = sv_hi(u.x);
-  x[2] = sv_lo(u.y); x[3] = sv_hi(u.y);
-  x[4] = sv_lo(u.z); x[5] = sv_hi(u.z);
-  x[6] = sv_lo(u.w); x[7] = sv_hi(u.w);
+__device__ __forceinline__ float2 two(uint32_t w) {
+  return make_float2(sv_lo(w), sv_hi(w));
 }
-__device__ __forceinline__ uint4 pack8f(const float* x) {
-  return make_uint4(sv_pack(x[0], x[1]), sv_pack(x[2], x[3]),
-                    sv_pack(x[4], x[5]), sv_pack(x[6], x[7]));
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+  return sv_pack(v.x, v.y);
 }
-__device__ __forceinline__ float round_bf16(float x) {
-  return sv_lo(sv_pack(x, 0.f));
+__device__ __forceinline__ const uint32_t* words(const uint4& u) {
+  return reinterpret_cast<const uint32_t*>(&u);
 }
 
-// LPH = d / 16 threads a head; HPT heads a thread.
-template <int LPH, int HPT>
-__global__ void __launch_bounds__(kThreadsA)
-    append_kernel(const __grid_constant__ AppendArgs a, int n_items, int HG) {
+// LPH = d / 16 threads a head; HS threads share a token's heads at one place.
+template <int LPH>
+__global__ void __launch_bounds__(kThreadsA, 2)
+    append_kernel(const __grid_constant__ AppendArgs a, int HS) {
   sv_grid_wait();
   const PagedArgs& p = a.p;
   constexpr int d = LPH * 16;
-  const int gt = blockIdx.x * kThreadsA + threadIdx.x;
-  const bool live = gt < n_items * LPH;
-  const int item = live ? gt / LPH : n_items - 1;
-  const int c = gt % LPH;
-  const int t = item / HG, hg = item - t * HG;
+  const int c = threadIdx.x % LPH, hs = threadIdx.x / LPH % HS;
+  const int n_tok = kThreadsA / (LPH * HS);
+  const int t = blockIdx.x * n_tok + threadIdx.x / (LPH * HS);
+  const bool row = t < p.n_tokens;
+  const int h0 = (a.q_out ? 0 : p.Hq) + hs;   // no query output: keys on
   const int H = p.Hq + 2 * p.Hkv;
   // the two chunks of this thread, in values
-  int lo, hi;
   const bool turns = c < a.rot / 16;
-  if (!turns || a.interleaved) {
-    lo = 16 * c;
-    hi = lo + 8;
-  } else {
-    lo = 8 * c;
-    hi = lo + a.rot / 2;
-  }
-  uint4 u0[HPT], u1[HPT];
-  const int h_first = a.q_out ? 0 : p.Hq;   // no query output: keys on
-#pragma unroll
-  for (int j = 0; j < HPT; ++j) {
-    const int h = h_first + hg + j * HG;
-    if (!live || h >= H) continue;
+  const int lo = !turns || a.interleaved ? 16 * c : 8 * c;
+  const int hi = !turns || a.interleaved ? lo + 8 : lo + a.rot / 2;
+  const uint16_t* rq = a.q + t * a.q_stride;
+  const uint16_t* rk = a.k + t * a.k_stride - (int64_t)p.Hq * d;
+  const uint16_t* rv = a.v + t * a.v_stride - (int64_t)(p.Hq + p.Hkv) * d;
+  auto fetch = [&](int h, uint4& u, uint4& v) {
+    if (!row || h >= H) return;
     const uint16_t* src =
-        h < p.Hq ? a.q + t * a.q_stride + (int64_t)h * d
-        : h < p.Hq + p.Hkv
-            ? a.k + t * a.k_stride + (int64_t)(h - p.Hq) * d
-            : a.v + t * a.v_stride + (int64_t)(h - p.Hq - p.Hkv) * d;
-    u0[j] = __ldg(reinterpret_cast<const uint4*>(src + lo));
-    u1[j] = __ldg(reinterpret_cast<const uint4*>(src + hi));
+        (h < p.Hq ? rq : h < p.Hq + p.Hkv ? rk : rv) + (int64_t)h * d;
+    u = __ldcs(reinterpret_cast<const uint4*>(src + lo));
+    v = __ldcs(reinterpret_cast<const uint4*>(src + hi));
+  };
+  uint4 u[2] = {}, v[2] = {};
+  fetch(h0, u[0], v[0]);
+  fetch(h0 + HS, u[1], v[1]);
+  // where the token goes: the warp finds the sequence of its first token,
+  // its others are a step or a few further
+  const int tw = min(__shfl_sync(0xffffffffu, t, 0), p.n_tokens - 1);
+  int b = sv_seq_of_warp(p.q_start, p.tokens_per_seq, p.batch, tw);
+  if (t != tw && row) {
+    if (p.q_start && b >= 0) {
+      while (b < p.batch && __ldg(p.q_start + b + 1) <= t) ++b;
+      if (b == p.batch) b = -1;
+    } else {
+      b = sv_seq_of(p.q_start, p.tokens_per_seq, p.batch, t);
+    }
   }
-  // where the token goes
-  const int b = sv_seq_of(p.q_start, p.tokens_per_seq, p.batch, t);
-  int pos = -1, page = -1;
-  bool ok = live && b >= 0;
+  bool ok = row && b >= 0;
+  int pos = 0;
+  int64_t slot = 0;
   if (ok) {
     pos = __ldg(p.seq_lens + b) + t -
           sv_row(p.q_start, p.tokens_per_seq, p.n_tokens, b);
     const int pi = pos >= 0 ? (int)sv_div(pos, p.page_div) : p.max_pages;
+    int page = -1;
     if (pi < p.max_pages)
       page = __ldg(p.page_table + (int64_t)b * p.max_pages + pi);
     if (page < 0 || page >= p.num_pages) {
@@ -85,86 +88,110 @@ __global__ void __launch_bounds__(kThreadsA)
       ok = false;
       sv_latch(p.status, MPK_ERR_INVALID_ARG);
     }
+    slot = ((int64_t)page * p.Hkv * p.page_size + (pos - pi * p.page_size)) * d;
   }
-  float cs[8], sn[8];
-  if (turns && ok) {
-    const float4* tab = reinterpret_cast<const float4*>(
-        a.table + ((int64_t)pos * (a.rot / 2) + 8 * c) * 2);
+  float2 cs[4], sn[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 w = __ldg(tab + i);
-      cs[2 * i] = w.x;
-      sn[2 * i] = w.y;
-      cs[2 * i + 1] = w.z;
-      sn[2 * i + 1] = w.w;
-    }
+  for (int i = 0; i < 4; ++i) {
+    float4 f = make_float4(1.f, 0.f, 1.f, 0.f);
+    if (turns && ok)
+      f = __ldg(reinterpret_cast<const float4*>(
+                    a.table + ((int64_t)pos * (a.rot / 2) + 8 * c) * 2) + i);
+    cs[i] = make_float2(f.x, f.z);
+    sn[i] = make_float2(f.y, f.w);
   }
-  const int64_t slot =
-      ok ? ((int64_t)page * p.Hkv * p.page_size + (pos % p.page_size)) * d : 0;
-#pragma unroll
-  for (int j = 0; j < HPT; ++j) {
-    const int h = h_first + hg + j * HG;
+  uint16_t* oq = a.q_out + t * a.q_out_stride;
+  const int64_t head = (int64_t)p.page_size * d;
+  const bool norms = a.q_norm || a.k_norm;
+  // one head: chunks x and y of it to its place
+  auto work = [&](int h, uint4 cu, uint4 cv) {
+    const bool here = ok && h < H;
     const bool isq = h < p.Hq, isk = !isq && h < p.Hq + p.Hkv;
     const uint16_t* nw = isq ? a.q_norm : isk ? a.k_norm : nullptr;
-    float x[8], y[8];
-    if (live && h < H) {
-      unpack8(u0[j], x);
-      unpack8(u1[j], y);
-    }
-    // The norm's output is a bf16 tensor of the decode step, so it is
-    // rounded here too: the cache holds what mpk_decode_step would write,
-    // bit for bit.  The sum of squares is fp32 over at most 128 values.
-    // Threads without a head of this pass join the shuffles.
-    float ss = 0.f;
-    if (a.q_norm || a.k_norm) {
-      if (live && h < H)
+    float2 x[4], y[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
+    for (int i = 0; i < 4; ++i) {
+      x[i] = two(words(cu)[i]);
+      y[i] = two(words(cv)[i]);
+    }
+    float r = 0.f;
+    if (norms) {
+      // The sum of squares is fp32 over at most 128 values; threads without
+      // a head of this turn join the shuffles.
+      float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        ss = __ffma2_rn(x[i], x[i], __ffma2_rn(y[i], y[i], ss));
+      float sum = ss.x + ss.y;
 #pragma unroll
       for (int o = LPH / 2; o > 0; o >>= 1)
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      r = 1.0f / sqrtf(sum / (float)d + a.eps);
     }
-    if (!ok || h >= H) continue;
+    if (!here) return;
     if (nw) {
-      const float r = 1.0f / sqrtf(ss / (float)d + a.eps);
-      float wa[8], wb[8];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(nw + lo)), wa);
-      unpack8(__ldg(reinterpret_cast<const uint4*>(nw + hi)), wb);
+      // The norm's output is a bf16 tensor of the decode step, so it is
+      // rounded here too: the cache holds what mpk_decode_step would write,
+      // bit for bit.
+      const uint4 wa = __ldg(reinterpret_cast<const uint4*>(nw + lo));
+      const uint4 wb = __ldg(reinterpret_cast<const uint4*>(nw + hi));
+      const float2 rr = make_float2(r, r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] = round_bf16(__fmul_rn(__fmul_rn(x[i], r), wa[i]));
-        y[i] = round_bf16(__fmul_rn(__fmul_rn(y[i], r), wb[i]));
+      for (int i = 0; i < 4; ++i) {
+        x[i] = two(pack2(__fmul2_rn(__fmul2_rn(x[i], rr), two(words(wa)[i]))));
+        y[i] = two(pack2(__fmul2_rn(__fmul2_rn(y[i], rr), two(words(wb)[i]))));
       }
     }
-    if (turns && (isq || isk)) {
+    const bool rot = turns && (isq || isk);
+    if (rot) {
+      const float2 m1 = make_float2(-1.f, -1.f);
       if (a.interleaved) {
+        // pairs lie side by side: (even, odd) of two values to (evens, odds)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float* z = i < 4 ? x + 2 * i : y + 2 * (i - 4);
-          const float e = z[0], o = z[1];
-          z[0] = __fsub_rn(__fmul_rn(e, cs[i]), __fmul_rn(o, sn[i]));
-          z[1] = __fadd_rn(__fmul_rn(o, cs[i]), __fmul_rn(e, sn[i]));
+        for (int i = 0; i < 4; ++i) {
+          float2* z = i < 2 ? x + 2 * i : y + 2 * (i - 2);
+          const float2 e = make_float2(z[0].x, z[1].x);
+          const float2 o = make_float2(z[0].y, z[1].y);
+          const float2 q =
+              __fadd2_rn(__fmul2_rn(e, cs[i]),
+                         __fmul2_rn(m1, __fmul2_rn(o, sn[i])));
+          const float2 w =
+              __fadd2_rn(__fmul2_rn(o, cs[i]), __fmul2_rn(e, sn[i]));
+          z[0] = make_float2(q.x, w.x);
+          z[1] = make_float2(q.y, w.y);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float e = x[i], o = y[i];
-          x[i] = __fsub_rn(__fmul_rn(e, cs[i]), __fmul_rn(o, sn[i]));
-          y[i] = __fadd_rn(__fmul_rn(o, cs[i]), __fmul_rn(e, sn[i]));
+        for (int i = 0; i < 4; ++i) {
+          const float2 e = x[i], o = y[i];
+          x[i] = __fadd2_rn(__fmul2_rn(e, cs[i]),
+                            __fmul2_rn(m1, __fmul2_rn(o, sn[i])));
+          y[i] = __fadd2_rn(__fmul2_rn(o, cs[i]), __fmul2_rn(e, sn[i]));
         }
       }
     }
-    uint16_t* dst;
-    if (isq)
-      dst = a.q_out + t * a.q_out_stride + (int64_t)h * d;
-    else if (isk)
-      dst = p.k + slot + (int64_t)(h - p.Hq) * p.page_size * d;
-    else
-      dst = p.v + slot + (int64_t)(h - p.Hq - p.Hkv) * p.page_size * d;
+    uint16_t* dst = isq   ? oq + (int64_t)h * d
+                    : isk ? p.k + slot + (h - p.Hq) * head
+                          : p.v + slot + (h - p.Hq - p.Hkv) * head;
     // untouched values keep their bits (NaN payloads among them)
-    const bool same = !nw && !(turns && (isq || isk));
-    *reinterpret_cast<uint4*>(dst + lo) = same ? u0[j] : pack8f(x);
-    *reinterpret_cast<uint4*>(dst + hi) = same ? u1[j] : pack8f(y);
+    if (nw || rot) {
+      cu = make_uint4(pack2(x[0]), pack2(x[1]), pack2(x[2]), pack2(x[3]));
+      cv = make_uint4(pack2(y[0]), pack2(y[1]), pack2(y[2]), pack2(y[3]));
+    }
+    *reinterpret_cast<uint4*>(dst + lo) = cu;
+    *reinterpret_cast<uint4*>(dst + hi) = cv;
+  };
+  // (the same number of turns for all threads of a warp)
+  for (int h = h0; h - hs < H; h += 2 * HS) {
+    uint4 nu[2] = {}, nv[2] = {};
+    fetch(h + 2 * HS, nu[0], nv[0]);
+    fetch(h + 3 * HS, nu[1], nv[1]);
+    work(h, u[0], v[0]);
+    work(h + HS, u[1], v[1]);
+    u[0] = nu[0];
+    u[1] = nu[1];
+    v[0] = nv[0];
+    v[1] = nv[1];
   }
 }
 
@@ -212,18 +239,18 @@ __global__ void rope_table_kernel(const __grid_constant__ RopeTableArgs a) {
 template <int LPH>
 cudaError_t append_d(const AppendArgs& a, cudaStream_t s) {
   const int H = (a.q_out ? a.p.Hq : 0) + 2 * a.p.Hkv;
-  // One head a thread while that fills the GPU at most once (the chain of
-  // loads is what such a call costs), else three.
-  const int64_t all = (int64_t)a.p.n_tokens * H * LPH;
-  const bool few = all <= 152 * 2048;
-  const int hpt = few ? 1 : 3;
-  const int HG = (H + hpt - 1) / hpt;
-  const int64_t items = (int64_t)a.p.n_tokens * HG;
-  const int64_t threads = items * LPH;
-  if (threads > 0x7fffffff) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)((threads + kThreadsA - 1) / kThreadsA));
-  auto k = few ? append_kernel<LPH, 1> : append_kernel<LPH, 3>;
-  return sv_launch(k, grid, kThreadsA, 0, s, true, a, (int)items, HG);
+  // Threads that share a token's heads: as many as there are heads while the
+  // call fills the GPU at most once (its cost is the chain of loads), else
+  // few, so that a thread's start serves many heads, but two waves of CTAs.
+  const int64_t T = a.p.n_tokens;
+  int HS = 1;
+  while (HS < 32 && HS * LPH < kThreadsA && HS < H &&
+         T * LPH * HS < (int64_t)152 * 512 * 2)
+    HS *= 2;
+  const int n_tok = kThreadsA / (LPH * HS);
+  return sv_launch(append_kernel<LPH>,
+                   dim3((unsigned)((T + n_tok - 1) / n_tok)), kThreadsA, 0, s,
+                   a, HS);
 }
 
 }  // namespace
@@ -239,7 +266,7 @@ cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t s) {
   const int64_t blocks = (n + 127) / 128;
   return sv_launch(rope_table_kernel,
                    dim3((unsigned)(blocks < 4096 ? blocks : 4096)), 128, 0, s,
-                   true, a);
+                   a);
 }
 
 }  // namespace mpk

@@ -171,8 +171,7 @@ template <int D>
 cudaError_t run_merge(const AttendArgs& a, cudaStream_t s) {
   const int64_t warps = (int64_t)a.p.n_tokens * a.p.Hq;
   const int64_t blocks = (warps + kNT / 32 - 1) / (kNT / 32);
-  return sv_launch(attend_merge<D>, dim3((unsigned)blocks), kNT, 0, s, true,
-                   a);
+  return sv_launch(attend_merge<D>, dim3((unsigned)blocks), kNT, 0, s, a);
 }
 
 }  // namespace

@@ -779,7 +779,7 @@ cudaError_t run_tiles(const AttendArgs& a, cudaStream_t s) {
       k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
   const int ctas = WMP > 1 ? 2 : Cfg<D>::kCtas;
-  return sv_launch(k, dim3(attend_ctas() / 4 * ctas), kNT, Cfg<D>::kSmem, s, true, a);
+  return sv_launch(k, dim3(attend_ctas() / 4 * ctas), kNT, Cfg<D>::kSmem, s, a);
 }
 
 template <int D>

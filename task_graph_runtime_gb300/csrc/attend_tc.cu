@@ -513,7 +513,7 @@ cudaError_t tc_d(const AttendArgs& a, cudaStream_t s) {
       TcSmem<D>::kSmem);
   if (e != cudaSuccess) return e;
   return sv_launch(attend_tc<D>, dim3(attend_tc_ctas()), kThreadsT,
-                   TcSmem<D>::kSmem, s, true, a);
+                   TcSmem<D>::kSmem, s, a);
 }
 
 }  // namespace

@@ -119,11 +119,11 @@ struct VerifyArgs {
   int32_t* seq_lens_out;
   uint32_t* status;
   // workspace
-  float2* stat;                // [2][n_tokens][splits] (maximum, sum)
-  int32_t* amax;               // [n_tokens][splits] index of the maximum
-  unsigned long long* race;    // [batch][2] packed (value, ~index)
+  float4* part;                // [2][n_tokens][slices]: target's, draft's
+                               // maximum, sum, index of the maximum
+  int slices;
+  unsigned long long* race;    // [batch] packed (value, ~index)
   uint32_t* arrived;           // [batch]
-  int splits;                  // slices of a row in the first pass
 };
 size_t verify_workspace(VerifyArgs* a, char* base);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);

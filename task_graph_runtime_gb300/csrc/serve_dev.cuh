@@ -62,13 +62,29 @@ __device__ __forceinline__ int sv_seq_of(const int32_t* q_start, int per,
   return lo;
 }
 
+// The same by a whole warp: the sequences that end at or before row t are
+// counted 32 at a time, one load's latency for all (a search takes one for
+// each halving).  Large batches are searched.
+__device__ __forceinline__ int sv_seq_of_warp(const int32_t* q_start, int per,
+                                              int batch, int t) {
+  if (!q_start || batch > 512) return sv_seq_of(q_start, per, batch, t);
+  if (t < __ldg(q_start)) return -1;
+  int n = 0;
+#pragma unroll 4
+  for (int b0 = 0; b0 < batch; b0 += 32) {
+    const int b = b0 + (int)(threadIdx.x & 31);
+    const bool done = b < batch && __ldg(q_start + b + 1) <= t;
+    n += __popc(__ballot_sync(0xffffffffu, done));
+  }
+  return n < batch ? n : -1;
+}
+
 // Launch with the attribute that lets the kernel's preamble overlap the end
 // of the kernel before it in the stream (which must call sv_grid_wait before
 // it touches what that kernel writes).
 template <typename... KArgs, typename... Args>
 inline cudaError_t sv_launch(void (*k)(KArgs...), dim3 grid, int threads,
-                             size_t smem, cudaStream_t s, bool overlap,
-                             Args... args) {
+                             size_t smem, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t c = {};
   c.gridDim = grid;
   c.blockDim = dim3(threads);
@@ -78,7 +94,7 @@ inline cudaError_t sv_launch(void (*k)(KArgs...), dim3 grid, int threads,
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = at;
-  c.numAttrs = overlap ? 1 : 0;
+  c.numAttrs = 1;
   return cudaLaunchKernelEx(&c, k, args...);
 }
 

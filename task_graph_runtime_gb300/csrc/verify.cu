@@ -10,18 +10,28 @@
 // so w needs no normalisation and no running sum over the vocabulary, and
 // the answer does not depend on the order of one (an inverse CDF's does).
 //
-// verify_stats: (maximum, sum of exponentials) of every row, a row cut into
-// slices so that few rows still fill the GPU; greedy rows (T <= 0) keep the
-// index of the maximum instead.  verify_sample: every CTA of a sequence joins
-// its rows' slices (in 64 bits), finds the first refused draft, and races its
-// slice of that one row; slices meet in one 64-bit atomic maximum of (value,
-// lowest index), whose result does not depend on their order.
+// verify_stats: maximum and sum of exponentials of every row and the drafted
+// token's logit; greedy rows (T <= 0) the index of the maximum.  A row is cut
+// into slices so that few rows still fill the GPU (joining them in a cluster
+// of CTAs took half as long again as leaving them to the second pass).
+// verify_sample: every CTA of a sequence joins its rows' slices (a warp a row,
+// in 64 bits), finds the first refused draft and races its slice of that one row; slices meet in one 64-bit atomic maximum of
+// (value, lowest index), whose result does not depend on their order.  Most
+// values of a slice cannot win: bounds from fast functions decide that, and
+// only the few above a warp's best lower bound are worked out exactly.
 // Bound by HBM: each row of logits leaves it once, the row that is sampled
 // from once more with its draft and noise rows.
 #include "serve_dev.cuh"
 
 namespace mpk {
 namespace {
+
+// A row of logits, its slices joined.
+struct VerifyRow {
+  double z;                    // sum of e^((x - m) / T)
+  float m;                     // maximum
+  int best;                    // its lowest index (greedy rows), or -1
+};
 
 constexpr int kNT = 256;
 constexpr int kMaxOut = 128;     // rows of a sequence
@@ -68,23 +78,12 @@ __global__ void __launch_bounds__(kNT)
          blockIdx.x) * kNT + tid;
     const int64_t all = (int64_t)gridDim.x * gridDim.y * gridDim.z * kNT;
     for (int64_t b = i; b < a.batch; b += all) {
-      a.race[2 * b] = a.race[2 * b + 1] = 0ull;
+      a.race[b] = 0ull;
       a.arrived[b] = 0u;
     }
   }
   const int row = blockIdx.y;
   if (row >= a.n_tokens) return;
-  const int b = sv_seq_of(a.q_start, a.tokens_per_seq, a.batch, row);
-  if (b < 0) return;
-  const float T = a.temperature ? __ldg(a.temperature + b) : 1.f;
-  const bool greedy = !(T > 0.f);
-  if (blockIdx.z == 1) {
-    // drafts' rows: the last row of a sequence has no draft after it, and a
-    // greedy sequence does not ask for their distribution
-    const RowInfo r = rows_of(a, b);
-    if (row == r.first + r.n - 1 || greedy) return;
-  }
-  const float c = greedy ? 1.f : kLog2e / T;
   const float* x = blockIdx.z ? a.draft + row * a.draft_stride
                               : a.logits + row * a.logits_stride;
   // vectors of four on 16-byte boundaries: vector v holds values
@@ -93,33 +92,48 @@ __global__ void __launch_bounds__(kNT)
   const int nv = (a.vocab + o + 3) / 4;
   const int v0 = (int)((int64_t)nv * blockIdx.x / gridDim.x);
   const int v1 = (int)((int64_t)nv * (blockIdx.x + 1) / gridDim.x);
-  float m = -INFINITY, z = 0.f;
-  int best = 0x7fffffff;
-  constexpr int U = 4;
-  for (int v = v0 + tid; v < v1; v += U * kNT) {
-    float4 w[U];
+  constexpr int U = 8;
+  float4 w[U];
+  auto fetch = [&](int v) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int vi = v + i * kNT, k = 4 * vi - o;
-      if (vi < v1 && k >= 0 && k + 4 <= a.vocab) {
-        w[i] = __ldcs(reinterpret_cast<const float4*>(x + k));
+      w[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (vi >= v1) continue;
+      if (k >= 0 && k + 4 <= a.vocab) {
+        w[i] = __ldg(reinterpret_cast<const float4*>(x + k));
       } else {
-        float q[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          q[j] = vi < v1 && k + j >= 0 && k + j < a.vocab ? x[k + j]
-                                                          : -INFINITY;
-        w[i] = make_float4(q[0], q[1], q[2], q[3]);
+        if (k >= 0) w[i].x = x[k];
+        if (k + 1 >= 0 && k + 1 < a.vocab) w[i].y = x[k + 1];
+        if (k + 2 >= 0 && k + 2 < a.vocab) w[i].z = x[k + 2];
+        if (k + 3 < a.vocab) w[i].w = x[k + 3];
       }
+    }
+  };
+  fetch(v0 + tid);     // on the way while the sequence is looked up
+  const int b = sv_seq_of_warp(a.q_start, a.tokens_per_seq, a.batch, row);
+  if (b < 0) return;
+  const float T = a.temperature ? __ldg(a.temperature + b) : 1.f;
+  const bool greedy = !(T > 0.f);
+  const RowInfo ri = rows_of(a, b);
+  const bool judges = row < ri.first + ri.n - 1;   // a draft comes after it
+  // drafts' rows: none after the last draft, and a greedy sequence does not
+  // ask for their distribution
+  if (blockIdx.z == 1 && (!judges || greedy)) return;
+  const float c = greedy ? 1.f : kLog2e / T;
+  float m = -INFINITY, z = 0.f;
+  int best = 0x7fffffff;
+  for (int v = v0 + tid; v < v1; v += U * kNT) {
+    if (v != v0 + tid) fetch(v);
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
       w[i].x = clean(w[i].x);
       w[i].y = clean(w[i].y);
       w[i].z = clean(w[i].z);
       w[i].w = clean(w[i].w);
-    }
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < U; ++i)
       top = fmaxf(top, fmaxf(fmaxf(w[i].x, w[i].y), fmaxf(w[i].z, w[i].w)));
+    }
     if (greedy) {
       if (top > m) {
         m = top;
@@ -178,8 +192,7 @@ __global__ void __launch_bounds__(kNT)
     for (int w = 1; w < kNT / 32; ++w) fold(sm[w], sz[w], sb[w]);
     const int64_t at =
         ((int64_t)blockIdx.z * a.n_tokens + row) * gridDim.x + blockIdx.x;
-    a.stat[at] = make_float2(m, z);
-    if (blockIdx.z == 0) a.amax[at] = best;
+    a.part[at] = make_float4(m, z, __int_as_float(best), 0.f);
   }
 }
 
@@ -216,180 +229,266 @@ __device__ __forceinline__ unsigned long long race_key(float v, int i) {
          (0xffffffffu - (uint32_t)i);
 }
 
+// Bounds of the weights leave room for fast functions: an exponent off by
+// 126 x 2^-22 at most, ex2 and a reciprocal good to 2^-22.
+constexpr float kUp = 1.f + 0x1p-14f, kDown = 1.f - 0x1p-14f;
+
+// What a slice needs to know of the row that is sampled from.
+struct Race {
+  const float *x, *y, *e;      // logits, draft (or null), noise
+  float m, iz, mq, izq;        // the rows' maxima and reciprocal sums
+  float ch, cl;                // log2(e) / T in two parts
+  int skip;                    // token whose weight is 0 (or -1)
+  bool dlog;
+};
+__device__ __forceinline__ unsigned long long race_exact(const Race& r, int v,
+                                                         bool residual) {
+  const float p = weight(clean(r.x[v]), r.m, r.ch, r.cl) * r.iz;
+  float w = p;
+  if (residual && r.y) {
+    const float y = r.y[v];
+    w = p - (!r.dlog ? y
+             : r.mq == -INFINITY
+                 ? 0.f
+                 : weight(clean(y), r.mq, r.ch, r.cl) * r.izq);
+  } else if (residual && v == r.skip) {
+    w = 0.f;
+  }
+  const float s = w / r.e[v];
+  return w > 0.f && s >= 0.f ? race_key(s, v) : 0ull;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// e^((x - m) / T) roughly (1 where x is m, which may be infinite)
+__device__ __forceinline__ float rough(float x, float m, float c) {
+  return x == m ? 1.f : ex2a((x - m) * c);
+}
+
+// The whole row, weight p alone: for a residual that is nowhere positive (p
+// and q agree to the last bit), a rare case left to one CTA.
+__device__ __noinline__ unsigned long long race_plain(const Race& r,
+                                                      int vocab) {
+  __shared__ unsigned long long s_k[kNT / 32];
+  unsigned long long k = 0;
+  for (int v = threadIdx.x; v < vocab; v += kNT)
+    k = max(k, race_exact(r, v, false));
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1)
+    k = max(k, __shfl_xor_sync(0xffffffffu, k, s));
+  if ((threadIdx.x & 31) == 0) s_k[threadIdx.x >> 5] = k;
+  __syncthreads();
+  for (int w = 0; w < kNT / 32; ++w) k = max(k, s_k[w]);
+  return k;
+}
+
+// KIND: 0 weights p, 1 p - q with probabilities q, 2 p - q with logits q,
+// 3 p without one token.  VEC: the rows lie on the same 16-byte phase.
+template <int KIND, bool VEC>
+__device__ __forceinline__ unsigned long long race_slice(const Race& r,
+                                                         int vocab) {
+  const int tid = threadIdx.x;
+  constexpr bool Q = KIND == 1 || KIND == 2;
+  constexpr int U = 4;                 // vectors of four a turn
+  const int o = VEC ? (int)(((uintptr_t)r.x >> 2) & 3) : 0;
+  const int nv = (vocab + o + 3) / 4;
+  const int v0 = (int)((int64_t)nv * blockIdx.x / gridDim.x);
+  const int v1 = (int)((int64_t)nv * (blockIdx.x + 1) / gridDim.x);
+  unsigned long long best = 0ull;
+  float floor_ = 0.f;                  // the best is at least this
+  for (int v = v0; v < v1; v += U * kNT) {
+    float up[4 * U];
+    float low = 0.f;
+    // value j of vector i: 4 (v + i kNT + tid) - o + j, or without a common
+    // phase 4 (v + i kNT) + j kNT + tid, in either case this thread's own
+    float x[4 * U], y[4 * U], e[4 * U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int vi = v + i * kNT + tid, k = 4 * vi - o;
+      if (VEC && vi < v1 && k >= 0 && k + 4 <= vocab) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(r.x + k));
+        const float4 b = __ldcs(reinterpret_cast<const float4*>(r.e + k));
+        x[4 * i] = a.x; x[4 * i + 1] = a.y; x[4 * i + 2] = a.z; x[4 * i + 3] = a.w;
+        e[4 * i] = b.x; e[4 * i + 1] = b.y; e[4 * i + 2] = b.z; e[4 * i + 3] = b.w;
+        if (Q) {
+          const float4 q = __ldg(reinterpret_cast<const float4*>(r.y + k));
+          y[4 * i] = q.x; y[4 * i + 1] = q.y; y[4 * i + 2] = q.z; y[4 * i + 3] = q.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int q = VEC ? k + j : 4 * (v + i * kNT) + j * kNT + tid;
+          const bool in = VEC ? vi < v1 && q >= 0 && q < vocab
+                              : q < min(4 * v1, vocab);
+          x[4 * i + j] = in ? __ldg(r.x + q) : -INFINITY;
+          e[4 * i + j] = in ? __ldcs(r.e + q) : 1.f;
+          if (Q) y[4 * i + j] = in ? __ldg(r.y + q) : 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * U; ++i) {
+      const float p = rough(clean(x[i]), r.m, r.ch) * r.iz;
+      const float t = rcp(e[i]);
+      float a = p * kUp, b = p * kDown;
+      if (Q) {
+        const float q = KIND == 1 ? y[i]
+                                  : rough(clean(y[i]), r.mq, r.ch) * r.izq;
+        a = fmaf(q, -kDown, a);
+        b = fmaf(q, -kUp, b);
+      }
+      if (KIND == 3) {
+        const int k = VEC ? 4 * (v + (i / 4) * kNT + tid) - o + i % 4
+                          : 4 * (v + (i / 4) * kNT) + (i % 4) * kNT + tid;
+        if (k == r.skip) a = b = 0.f;
+      }
+      // (a NaN compares false below and bounds nothing)
+      up[i] = a * t * kUp;
+      low = fmaxf(low, b * t * kDown);
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1)
+      low = fmaxf(low, __shfl_xor_sync(0xffffffffu, low, s));
+    floor_ = fmaxf(floor_, low);
+    uint32_t mask = 0;
+#pragma unroll
+    for (int i = 0; i < 4 * U; ++i)
+      if (up[i] > 0.f && up[i] >= floor_) mask |= 1u << i;
+    while (mask) {
+      const int i = __ffs(mask) - 1;
+      mask &= mask - 1;
+      const int k = VEC ? 4 * (v + (i / 4) * kNT + tid) - o + i % 4
+                        : 4 * (v + (i / 4) * kNT) + (i % 4) * kNT + tid;
+      best = max(best, race_exact(r, k, KIND != 0));
+    }
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1)
+    best = max(best, __shfl_xor_sync(0xffffffffu, best, s));
+  return best;
+}
+
 __global__ void __launch_bounds__(kNT)
     verify_sample(const __grid_constant__ VerifyArgs a) {
-  __shared__ float s_m[2][kMaxOut];       // row maxima: target, draft
-  __shared__ double s_z[2][kMaxOut];      // row sums
-  __shared__ int s_best[kMaxOut];
-  __shared__ int s_ok[kMaxOut];           // 1 accepted, 0 refused, 2 no draft
+  __shared__ VerifyRow s_row[2][kMaxOut];
+  __shared__ int s_stop;       // first draft that is not accepted
   __shared__ int s_last;
-  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31,
-            warp = tid >> 5;
-  sv_grid_wait();
+  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  // (verify_stats has waited for what comes before it)
   RowInfo r = rows_of(a, b);
+  const float T = a.temperature ? __ldg(a.temperature + b) : 1.f;
   if (r.n > a.max_out) {
     if (tid == 0) sv_latch(a.status, MPK_ERR_INVALID_ARG);
     r.n = a.max_out;
   }
-  const float T = a.temperature ? __ldg(a.temperature + b) : 1.f;
   const bool greedy = !(T > 0.f);
   const float c = greedy ? 1.f : kLog2e / T;
   const bool dlog = a.draft && a.draft_is_logits;
-  // ---- the rows' statistics, and each draft's verdict
-  for (int i = warp; i < r.n; i += kNT / 32) {
+  if (tid == 0) s_stop = r.n - 1;
+  // the rows' slices, a warp a row; lane 0 has what judges the draft ready
+  bool waited = false;
+  for (int i = tid >> 5; i < r.n; i += kNT / 32) {
+    const int row = r.first + i;
+    const int d = i < r.n - 1 ? a.tokens[row + 1] : -1;
+    const bool have = d >= 0 && d < a.vocab;
+    float xd = 0.f, yd = 1.f, u = 0.f;
+    if (have && !greedy) {
+      xd = clean(a.logits[row * a.logits_stride + d]);
+      if (a.draft) yd = a.draft[row * a.draft_stride + d];
+      u = a.uniform[row];
+    }
+    if (!waited) sv_grid_wait();
+    waited = true;
+    double pq[2] = {0.0, (double)yd};    // of the drafted token
+    int best = -1;
     for (int k = 0; k < (dlog && !greedy && i < r.n - 1 ? 2 : 1); ++k) {
-      const int64_t at =
-          ((int64_t)k * a.n_tokens + r.first + i) * a.splits;
+      const float4* part =
+          a.part + ((int64_t)k * a.n_tokens + row) * a.slices;
       float m = -INFINITY;
-      int best = 0x7fffffff;
-      for (int s = lane; s < a.splits; s += 32) {
-        const float v = a.stat[at + s].x;
-        if (greedy && v > m) best = a.amax[at + s];
-        m = fmaxf(m, v);
+      int bi = 0x7fffffff;
+      for (int s = lane; s < a.slices; s += 32) {
+        const float4 v = part[s];
+        if (v.x > m) bi = __float_as_int(v.z);
+        m = fmaxf(m, v.x);
       }
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) {
         const float m2 = __shfl_xor_sync(0xffffffffu, m, s);
-        const int b2 = __shfl_xor_sync(0xffffffffu, best, s);
-        if (m2 > m || (m2 == m && b2 < best)) best = b2;
+        const int b2 = __shfl_xor_sync(0xffffffffu, bi, s);
+        if (m2 > m || (m2 == m && b2 < bi)) bi = b2;
         m = fmaxf(m, m2);
       }
       double z = 0.0;
-      for (int s = lane; s < a.splits; s += 32) {
-        const float2 v = a.stat[at + s];
+      for (int s = lane; s < a.slices; s += 32) {
+        const float4 v = part[s];
         z += (double)v.y * (v.x == m ? 1.0 : (double)ex2a((v.x - m) * c));
       }
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1)
         z += __shfl_xor_sync(0xffffffffu, z, s);
+      if (k == 0) best = m == -INFINITY ? -1 : bi;
       if (lane == 0) {
-        s_m[k][i] = m;
-        s_z[k][i] = z;
-        if (k == 0) s_best[i] = m == -INFINITY ? -1 : best;
-      }
-    }
-    __syncwarp();
-    if (lane == 0) {
-      const int row = r.first + i;
-      const int d = i < r.n - 1 ? a.tokens[row + 1] : -1;
-      int ok = 2;
-      if (d >= 0 && d < a.vocab) {
-        if (greedy) {
-          ok = d == s_best[i];
-        } else {
-          const float x = clean(a.logits[row * a.logits_stride + d]);
-          const double p =
-              s_m[0][i] == -INFINITY ? 0.0
-              : x == s_m[0][i]       ? 1.0 / s_z[0][i]
-                                     : exp(((double)x - s_m[0][i]) / T) /
-                                     s_z[0][i];
-          double q = 1.0;
-          if (a.draft) {
-            const float y = a.draft[row * a.draft_stride + d];
-            if (!dlog) q = y;
-            else if (s_m[1][i] == -INFINITY) q = 0.0;
-            else if (clean(y) == s_m[1][i]) q = 1.0 / s_z[1][i];
-            else q = exp(((double)clean(y) - s_m[1][i]) / T) / s_z[1][i];
-          }
-          ok = (double)a.uniform[row] * q < p ? 1 : 0;
+        s_row[k][i].z = z;
+        s_row[k][i].m = m;
+        s_row[k][i].best = best;
+        if (have && !greedy) {
+          const float at = k ? clean(yd) : xd;
+          pq[k] = m == -INFINITY ? 0.0
+                  : at == m      ? 1.0 / z
+                                 : exp(((double)at - m) / T) / z;
         }
       }
-      s_ok[i] = ok;
+    }
+    if (lane == 0 && i < r.n - 1) {
+      const bool ok =
+          have && (greedy ? best == d : (double)u * pq[1] < pq[0]);
+      if (!ok) atomicMin(&s_stop, i);
     }
   }
+  if (!waited) sv_grid_wait();
   __syncthreads();
-  int n_acc = 0;
-  while (n_acc < r.n - 1 && s_ok[n_acc] == 1) ++n_acc;
+  const int n_acc = max(s_stop, 0);
   const int row = r.first + n_acc;
-  const bool residual = n_acc < r.n && s_ok[n_acc] == 0;
+  const int refused = n_acc < r.n - 1 ? a.tokens[row + 1] : -1;
+  const bool residual = refused >= 0 && refused < a.vocab;
   // ---- this slice of the race
+  Race g;
   if (r.n > 0 && !greedy) {
-    const float m = s_m[0][n_acc];
-    const float iz = (float)(1.0 / s_z[0][n_acc]);
+    const VerifyRow w = s_row[0][n_acc];
     const double cd = 1.4426950408889634074 / (double)T;
-    const float ch = (float)cd, cl = (float)(cd - (double)ch);
-    const float* x = a.logits + row * a.logits_stride;
-    const float* e = a.noise + b * a.noise_stride;
-    const bool with_q = residual && a.draft;
-    const float* y = with_q ? a.draft + row * a.draft_stride : x;
-    const float mq = with_q && dlog ? s_m[1][n_acc] : 0.f;
-    const float izq = with_q && dlog ? (float)(1.0 / s_z[1][n_acc]) : 0.f;
-    const int skip = residual && !a.draft ? a.tokens[row + 1] : -1;
-    unsigned long long best = 0ull, plain = 0ull;
-    auto one = [&](int v, float xv, float yv, float ev) {
-      if (m == -INFINITY) return;
-      const float p = weight(clean(xv), m, ch, cl) * iz;
-      float w = p;
-      if (with_q) {
-        const float q = !dlog ? yv
-                        : mq == -INFINITY
-                            ? 0.f
-                            : weight(clean(yv), mq, ch, cl) * izq;
-        w = p - q;
-      } else if (v == skip) {
-        w = 0.f;
-      }
-      if (w > 0.f) {
-        const float s = w / ev;
-        if (s >= 0.f) best = max(best, race_key(s, v));
-      }
-      if (residual && p > 0.f) {
-        const float s = p / ev;
-        if (s >= 0.f) plain = max(plain, race_key(s, v));
-      }
-    };
-    const int o = (int)(((uintptr_t)x >> 2) & 3);
-    const bool same = (((uintptr_t)e >> 2) & 3) == (unsigned)o &&
-                      (((uintptr_t)y >> 2) & 3) == (unsigned)o;
-    if (same) {
-      const int nv = (a.vocab + o + 3) / 4;
-      const int v0 = (int)((int64_t)nv * blockIdx.x / gridDim.x);
-      const int v1 = (int)((int64_t)nv * (blockIdx.x + 1) / gridDim.x);
-      for (int v = v0 + tid; v < v1; v += kNT) {
-        const int k = 4 * v - o;
-        if (k >= 0 && k + 4 <= a.vocab) {
-          const float4 xv = __ldg(reinterpret_cast<const float4*>(x + k));
-          const float4 ev = __ldcs(reinterpret_cast<const float4*>(e + k));
-          const float4 yv =
-              with_q ? __ldg(reinterpret_cast<const float4*>(y + k)) : xv;
-          one(k, xv.x, yv.x, ev.x);
-          one(k + 1, xv.y, yv.y, ev.y);
-          one(k + 2, xv.z, yv.z, ev.z);
-          one(k + 3, xv.w, yv.w, ev.w);
-        } else {
-          for (int j = 0; j < 4; ++j)
-            if (k + j >= 0 && k + j < a.vocab)
-              one(k + j, x[k + j], y[k + j], e[k + j]);
-        }
-      }
-    } else {
-      // rows on different 16-byte phases (an odd vocabulary)
-      const int v0 = (int)((int64_t)a.vocab * blockIdx.x / gridDim.x);
-      const int v1 = (int)((int64_t)a.vocab * (blockIdx.x + 1) / gridDim.x);
-      constexpr int U = 4;
-      for (int v = v0 + tid; v < v1; v += U * kNT) {
-        float xv[U], yv[U], ev[U];
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-          const int k = min(v + j * kNT, v1 - 1);
-          xv[j] = __ldg(x + k);
-          ev[j] = __ldcs(e + k);
-          yv[j] = with_q ? __ldg(y + k) : 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-          if (v + j * kNT < v1) one(v + j * kNT, xv[j], yv[j], ev[j]);
-      }
+    g.x = a.logits + row * a.logits_stride;
+    g.e = a.noise + b * a.noise_stride;
+    g.y = residual && a.draft ? a.draft + row * a.draft_stride : nullptr;
+    g.m = w.m;
+    g.iz = (float)(1.0 / w.z);
+    g.ch = (float)cd;
+    g.cl = (float)(cd - (double)g.ch);
+    g.skip = residual && !a.draft ? refused : -1;
+    g.dlog = dlog;
+    g.mq = g.izq = 0.f;
+    if (g.y && dlog) {
+      const VerifyRow y = s_row[1][n_acc];
+      g.mq = y.m;
+      g.izq = y.m == -INFINITY ? 0.f : (float)(1.0 / y.z);
     }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
-      best = max(best, __shfl_xor_sync(0xffffffffu, best, s));
-      plain = max(plain, __shfl_xor_sync(0xffffffffu, plain, s));
+    unsigned long long best = 0ull;
+    if (g.m > -INFINITY) {
+      const unsigned o = ((uintptr_t)g.x >> 2) & 3;
+      const bool same = (((uintptr_t)g.e >> 2) & 3) == o &&
+                        (!g.y || (((uintptr_t)g.y >> 2) & 3) == o);
+      if (g.y && dlog)
+        best = same ? race_slice<2, true>(g, a.vocab)
+                    : race_slice<2, false>(g, a.vocab);
+      else if (g.y)
+        best = same ? race_slice<1, true>(g, a.vocab)
+                    : race_slice<1, false>(g, a.vocab);
+      else
+        best = same ? race_slice<3, true>(g, a.vocab)
+                    : race_slice<3, false>(g, a.vocab);
     }
-    if (lane == 0) {
-      if (best) atomicMax(a.race + 2 * b, best);
-      if (plain) atomicMax(a.race + 2 * b + 1, plain);
-    }
+    if (lane == 0 && best) atomicMax(a.race + b, best);
   }
   // ---- the last slice to finish writes the answer
   __threadfence();
@@ -401,11 +500,10 @@ __global__ void __launch_bounds__(kNT)
   int token = -1;
   if (r.n > 0) {
     if (greedy) {
-      token = s_best[n_acc];
+      token = s_row[0][n_acc].best;
     } else {
-      unsigned long long k = __ldcg(a.race + 2 * b);
-      // nothing of p lies above q (they agree to the last bit): sample p
-      if (k == 0ull) k = __ldcg(a.race + 2 * b + 1);
+      unsigned long long k = __ldcg(a.race + b);
+      if (k == 0ull && residual && g.m > -INFINITY) k = race_plain(g, a.vocab);
       if (k) token = (int)(0xffffffffu - (uint32_t)k);
     }
   }
@@ -419,10 +517,11 @@ __global__ void __launch_bounds__(kNT)
     if (a.logprobs) {
       float lp = 0.f;
       if (t >= 0 && !greedy) {
+        const VerifyRow w = s_row[0][i];
         const float x =
             clean(a.logits[(r.first + i) * a.logits_stride + t]);
-        const double d = x == s_m[0][i] ? 0.0 : (double)x - s_m[0][i];
-        lp = (float)(d / T - log(s_z[0][i]));
+        const double dx = x == w.m ? 0.0 : (double)x - w.m;
+        lp = (float)(dx / T - log(w.z));
       }
       a.logprobs[(int64_t)b * a.max_out + i] = lp;
     }
@@ -436,6 +535,15 @@ __global__ void __launch_bounds__(kNT)
   }
 }
 
+// Slices of a row in the first pass: at most 16384 values, fewer when there
+// are few rows (about four CTAs an SM), 2048 at least.
+int row_slices(const VerifyArgs& a) {
+  const int64_t rows = a.n_tokens > 0 ? a.n_tokens : 1;
+  int64_t s = (152 * 4 + rows - 1) / rows;
+  const int64_t lo = (a.vocab + 16383) / 16384, hi = (a.vocab + 2047) / 2048;
+  return (int)(s < lo ? lo : s > hi ? hi : s);
+}
+
 }  // namespace
 
 size_t verify_workspace(VerifyArgs* a, char* base) {
@@ -445,16 +553,10 @@ size_t verify_workspace(VerifyArgs* a, char* base) {
     off += (bytes + 255) / 256 * 256;
     return p;
   };
-  // Slices of at most 16384 values, fewer when there are few rows (about
-  // four CTAs an SM), and no fewer than 2048.
-  const int64_t rows = a->n_tokens > 0 ? a->n_tokens : 1;
-  int64_t s = (152 * 4 + rows - 1) / rows;
-  const int64_t lo = (a->vocab + 16383) / 16384, hi = (a->vocab + 2047) / 2048;
-  s = s < lo ? lo : s > hi ? hi : s;
-  a->splits = (int)s;
-  a->stat = reinterpret_cast<float2*>(take((size_t)2 * rows * s * 8));
-  a->amax = reinterpret_cast<int32_t*>(take((size_t)rows * s * 4));
-  a->race = reinterpret_cast<unsigned long long*>(take((size_t)a->batch * 16));
+  const size_t rows = a->n_tokens > 0 ? a->n_tokens : 1;
+  a->slices = row_slices(*a);
+  a->part = reinterpret_cast<float4*>(take(2 * rows * a->slices * 16));
+  a->race = reinterpret_cast<unsigned long long*>(take((size_t)a->batch * 8));
   a->arrived = reinterpret_cast<uint32_t*>(take((size_t)a->batch * 4));
   return off;
 }
@@ -462,14 +564,14 @@ size_t verify_workspace(VerifyArgs* a, char* base) {
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
   const int rows = a.n_tokens > 0 ? a.n_tokens : 1;
   const bool dlog = a.draft && a.draft_is_logits;
-  cudaError_t e = sv_launch(verify_stats, dim3(a.splits, rows, dlog ? 2 : 1),
-                            kNT, 0, s, true, a);
+  cudaError_t e = sv_launch(verify_stats, dim3(a.slices, rows, dlog ? 2 : 1),
+                            kNT, 0, s, a);
   if (e != cudaSuccess) return e;
+  // slices of a race: the same rule, 4096 values (one turn) at least
   int64_t n = (152 * 4 + a.batch - 1) / a.batch;
-  const int64_t hi = (a.vocab + 2047) / 2048;
+  const int64_t hi = (a.vocab + 4095) / 4096;
   n = n > hi ? hi : n;
-  return sv_launch(verify_sample, dim3((unsigned)n, a.batch), kNT, 0, s, true,
-                   a);
+  return sv_launch(verify_sample, dim3((unsigned)n, a.batch), kNT, 0, s, a);
 }
 
 }  // namespace mpk
