@@ -14,8 +14,9 @@
 // token's logit; greedy rows (T <= 0) the index of the maximum.  A row is cut
 // into slices so that few rows still fill the GPU (joining them in a cluster
 // of CTAs took half as long again as leaving them to the second pass).
-// verify_sample: every CTA of a sequence joins its rows' slices (a warp a row,
-// in 64 bits), finds the first refused draft and races its slice of that one row; slices meet in one 64-bit atomic maximum of
+// verify_sample: every CTA of a sequence joins its rows' slices (a warp a
+// row; in fp32: the FP64 units are few, and 64-bit sums here cost 10 us a
+// launch), finds the first refused draft and races its slice of that one row; slices meet in one 64-bit atomic maximum of
 // (value, lowest index), whose result does not depend on their order.  Most
 // values of a slice cannot win: bounds from fast functions decide that, and
 // only the few above a warp's best lower bound are worked out exactly.
@@ -28,14 +29,16 @@ namespace {
 
 // A row of logits, its slices joined.
 struct VerifyRow {
-  double z;                    // sum of e^((x - m) / T)
+  float z;                     // sum of e^((x - m) / T)
   float m;                     // maximum
   int best;                    // its lowest index (greedy rows), or -1
 };
 
 constexpr int kNT = 256;
 constexpr int kMaxOut = 128;     // rows of a sequence
+// log2(e) rounded to fp32, and the rest of it
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eLow = (float)(1.4426950408889634074 - (double)kLog2e);
 
 __device__ __forceinline__ float ex2a(float x) {
   float y;
@@ -92,9 +95,9 @@ __global__ void __launch_bounds__(kNT)
   const int nv = (a.vocab + o + 3) / 4;
   const int v0 = (int)((int64_t)nv * blockIdx.x / gridDim.x);
   const int v1 = (int)((int64_t)nv * (blockIdx.x + 1) / gridDim.x);
-  constexpr int U = 8;
-  float4 w[U];
-  auto fetch = [&](int v) {
+  constexpr int U = 4;
+  float4 w[U], next[U];
+  auto fetch = [&](int v, float4 (&w)[U]) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int vi = v + i * kNT, k = 4 * vi - o;
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(kNT)
       }
     }
   };
-  fetch(v0 + tid);     // on the way while the sequence is looked up
+  fetch(v0 + tid, w);  // on the way while the sequence is looked up
   const int b = sv_seq_of_warp(a.q_start, a.tokens_per_seq, a.batch, row);
   if (b < 0) return;
   const float T = a.temperature ? __ldg(a.temperature + b) : 1.f;
@@ -124,7 +127,10 @@ __global__ void __launch_bounds__(kNT)
   float m = -INFINITY, z = 0.f;
   int best = 0x7fffffff;
   for (int v = v0 + tid; v < v1; v += U * kNT) {
-    if (v != v0 + tid) fetch(v);
+    if (v != v0 + tid)
+#pragma unroll
+      for (int i = 0; i < U; ++i) w[i] = next[i];
+    fetch(v + U * kNT, next);
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -386,6 +392,9 @@ __global__ void __launch_bounds__(kNT)
   const bool greedy = !(T > 0.f);
   const float c = greedy ? 1.f : kLog2e / T;
   const bool dlog = a.draft && a.draft_is_logits;
+  // log2(e) / T in two parts
+  const float ch = greedy ? 1.f : kLog2e / T;
+  const float cl = greedy ? 0.f : (fmaf(-ch, T, kLog2e) + kLog2eLow) / T;
   if (tid == 0) s_stop = r.n - 1;
   // the rows' slices, a warp a row; lane 0 has what judges the draft ready
   bool waited = false;
@@ -401,7 +410,7 @@ __global__ void __launch_bounds__(kNT)
     }
     if (!waited) sv_grid_wait();
     waited = true;
-    double pq[2] = {0.0, (double)yd};    // of the drafted token
+    float pq[2] = {0.f, yd};             // of the drafted token
     int best = -1;
     for (int k = 0; k < (dlog && !greedy && i < r.n - 1 ? 2 : 1); ++k) {
       const float4* part =
@@ -420,10 +429,10 @@ __global__ void __launch_bounds__(kNT)
         if (m2 > m || (m2 == m && b2 < bi)) bi = b2;
         m = fmaxf(m, m2);
       }
-      double z = 0.0;
+      float z = 0.f;
       for (int s = lane; s < a.slices; s += 32) {
         const float4 v = part[s];
-        z += (double)v.y * (v.x == m ? 1.0 : (double)ex2a((v.x - m) * c));
+        z += v.y * (v.x == m ? 1.f : ex2a((v.x - m) * c));
       }
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1)
@@ -433,17 +442,13 @@ __global__ void __launch_bounds__(kNT)
         s_row[k][i].z = z;
         s_row[k][i].m = m;
         s_row[k][i].best = best;
-        if (have && !greedy) {
-          const float at = k ? clean(yd) : xd;
-          pq[k] = m == -INFINITY ? 0.0
-                  : at == m      ? 1.0 / z
-                                 : exp(((double)at - m) / T) / z;
-        }
+        if (have && !greedy)
+          pq[k] = m == -INFINITY ? 0.f
+                                 : weight(k ? clean(yd) : xd, m, ch, cl) / z;
       }
     }
     if (lane == 0 && i < r.n - 1) {
-      const bool ok =
-          have && (greedy ? best == d : (double)u * pq[1] < pq[0]);
+      const bool ok = have && (greedy ? best == d : u * pq[1] < pq[0]);
       if (!ok) atomicMin(&s_stop, i);
     }
   }
@@ -457,21 +462,20 @@ __global__ void __launch_bounds__(kNT)
   Race g;
   if (r.n > 0 && !greedy) {
     const VerifyRow w = s_row[0][n_acc];
-    const double cd = 1.4426950408889634074 / (double)T;
     g.x = a.logits + row * a.logits_stride;
     g.e = a.noise + b * a.noise_stride;
     g.y = residual && a.draft ? a.draft + row * a.draft_stride : nullptr;
     g.m = w.m;
-    g.iz = (float)(1.0 / w.z);
-    g.ch = (float)cd;
-    g.cl = (float)(cd - (double)g.ch);
+    g.iz = 1.f / w.z;
+    g.ch = ch;
+    g.cl = cl;
     g.skip = residual && !a.draft ? refused : -1;
     g.dlog = dlog;
     g.mq = g.izq = 0.f;
     if (g.y && dlog) {
       const VerifyRow y = s_row[1][n_acc];
       g.mq = y.m;
-      g.izq = y.m == -INFINITY ? 0.f : (float)(1.0 / y.z);
+      g.izq = y.m == -INFINITY ? 0.f : 1.f / y.z;
     }
     unsigned long long best = 0ull;
     if (g.m > -INFINITY) {
@@ -520,8 +524,7 @@ __global__ void __launch_bounds__(kNT)
         const VerifyRow w = s_row[0][i];
         const float x =
             clean(a.logits[(r.first + i) * a.logits_stride + t]);
-        const double dx = x == w.m ? 0.0 : (double)x - w.m;
-        lp = (float)(dx / T - log(w.z));
+        lp = (x == w.m ? 0.f : (x - w.m) / T) - logf(w.z);
       }
       a.logprobs[(int64_t)b * a.max_out + i] = lp;
     }
