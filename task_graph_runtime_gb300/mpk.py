@@ -463,13 +463,10 @@ def mpk_decode_step_noalloc(graph: "Graph", weights: Weights, tokens, kv,
 
 
 # ------------------------------------------------------- serving operators
-def _stream_of(stream, device):
-    import torch
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
+# These calls take a few microseconds on the GPU at small batches, so what
+# Python does around them counts: arguments are checked by value, the
+# structures that do not change are built once, and torch is asked for the
+# current device and stream by its shortest way.
 def _refuse(where: str, what: str):
     raise MpkError(MPK_ERR_INVALID_ARG, f"{where}: {what}")
 
@@ -477,10 +474,24 @@ def _refuse(where: str, what: str):
 class _OnDevice:
     """Calls go to the tensors' own device, whichever one is current."""
 
-    def _call(self, fn, *args):
+    def _on(self, device):
         import torch
-        if torch.cuda.current_device() == self.device.index:
+        self.device = device
+        self._index = device.index
+        self._bf16, self._f32, self._i32 = (torch.bfloat16, torch.float32,
+                                            torch.int32)
+        self._current = torch._C._cuda_getDevice
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
+
+    def _stream(self, stream):
+        if stream is None:
+            return self._raw_stream(self._index)
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+    def _call(self, fn, *args):
+        if self._current() == self._index:
             return fn(*args)
+        import torch
         with torch.cuda.device(self.device):
             return fn(*args)
 
@@ -488,7 +499,7 @@ class _OnDevice:
         """Device pointer of a contiguous vector of at least n values."""
         if t is None:
             return None
-        if (t.dtype is not dtype or t.device != self.device or
+        if (t.dtype is not dtype or t.get_device() != self._index or
                 t.numel() < n or not t.is_contiguous()):
             _refuse(where, f"{name} must be a contiguous {dtype} tensor of "
                            f"{n} values on {self.device}")
@@ -517,7 +528,9 @@ def mpk_rope_table(rotary_dim: int, n_pos: int, theta: float,
     with torch.cuda.device(dev):
         _check(load_library().mpk_rope_table(
             ctypes.byref(s), first_pos, n_pos, out.data_ptr() or None,
-            _stream_of(stream, dev)), "mpk_rope_table")
+            torch.cuda.current_stream(dev).cuda_stream if stream is None
+            else stream if isinstance(stream, int) else stream.cuda_stream),
+            "mpk_rope_table")
     return out
 
 
@@ -556,7 +569,7 @@ class PagedBatch(_OnDevice):
         import torch
         w = "PagedBatch"
         k, v = kv.k_pool, kv.v_pool
-        self.device = _cuda_device(k, w)
+        self._on(_cuda_device(k, w))
         if (k.dim() != 5 or k.dtype is not torch.bfloat16 or
                 v.dtype is not torch.bfloat16 or v.shape != k.shape or
                 not k.is_contiguous() or not v.is_contiguous() or
@@ -599,78 +612,84 @@ class PagedBatch(_OnDevice):
                       ctypes.byref(self._kv),
                       ctypes.byref(self._groups) if self._groups else None)
         self._ws = None
-        self._lib = load_library()
+        lib = load_library()
+        self._c_append, self._c_attend = (lib.mpk_kv_append,
+                                          lib.mpk_prefix_attention)
+        self._c_attend_ws = lib.mpk_prefix_attention_workspace
 
     def _rows(self, t, width, where, name):
         """Pointer and row stride of [n_tokens, width] (or [n_tokens, heads,
         head_dim]) bf16 rows whose values lie side by side."""
-        import torch
-        sh, n = t.shape, self.n_tokens
-        ok = t.dtype is torch.bfloat16 and t.device == self.device
+        sh, st, n = t.shape, t.stride(), self.n_tokens
+        ok = t.dtype is self._bf16 and t.get_device() == self._index
         if ok and len(sh) == 2:
-            ok = sh[0] >= n and sh[1] == width and t.stride(1) == 1
+            ok = sh[1] == width and st[1] == 1 and sh[0] >= n
         elif ok and len(sh) == 3:
             ok = (sh[0] >= n and sh[2] == self.head_dim and
-                  sh[1] * sh[2] == width and t.stride(2) == 1 and
-                  (sh[1] == 1 or t.stride(1) == sh[2]))
+                  sh[1] * sh[2] == width and st[2] == 1 and
+                  (sh[1] == 1 or st[1] == sh[2]))
         else:
             ok = False
         if not ok:
             _refuse(where, f"{name} must be bfloat16 [{n}, {width}] on "
                            f"{self.device} with contiguous rows")
-        return t.data_ptr(), (t.stride(0) if n > 1 else width)
-
-    def _layer(self, layer, where):
-        if not 0 <= layer < self.n_layers:
-            _refuse(where, f"layer {layer} of {self.n_layers}")
+        return t.data_ptr(), (st[0] if n > 1 else width)
 
     def append(self, layer: int, q, k, v, rope: Optional[Rope] = None,
                q_out=None, q_norm=None, k_norm=None, eps: float = 1e-6,
                stream=None):
         """mpk_kv_append: norm and rotate q and k, append k and v.  q may be
         None when q_out is."""
-        import torch
         w = "PagedBatch.append"
-        self._layer(layer, w)
-        if q_out is not None and q is None:
-            _refuse(w, "q_out without q")
-        qp = self._rows(q, self.q_width, w, "q") if q_out is not None \
-            else (None, 0)
-        kp = self._rows(k, self.kv_width, w, "k")
-        vp = self._rows(v, self.kv_width, w, "v")
-        op = self._rows(q_out, self.q_width, w, "q_out") \
-            if q_out is not None else (None, 0)
-        if rope is not None and rope.device != self.device:
-            _refuse(w, "rope is on another device")
-        d, bf = self.head_dim, torch.bfloat16
-        _check(self._call(
-            self._lib.mpk_kv_append, *self._refs[:3], layer, *qp, *kp, *vp,
-            self._vec(q_norm, d, bf, w, "q_norm"),
-            self._vec(k_norm, d, bf, w, "k_norm"), eps,
-            rope.ref if rope is not None else None, *op, self._st,
-            _stream_of(stream, self.device)), "mpk_kv_append")
+        if not 0 <= layer < self.n_layers:
+            _refuse(w, f"layer {layer} of {self.n_layers}")
+        kp, ks = self._rows(k, self.kv_width, w, "k")
+        vp, vs = self._rows(v, self.kv_width, w, "v")
+        qp = op = None
+        qs = os_ = 0
+        if q_out is not None:
+            if q is None:
+                _refuse(w, "q_out without q")
+            qp, qs = self._rows(q, self.q_width, w, "q")
+            op, os_ = self._rows(q_out, self.q_width, w, "q_out")
+        if rope is not None:
+            if rope.device != self.device:
+                _refuse(w, "rope is on another device")
+            rope = rope.ref
+        if q_norm is not None:
+            q_norm = self._vec(q_norm, self.head_dim, self._bf16, w, "q_norm")
+        if k_norm is not None:
+            k_norm = self._vec(k_norm, self.head_dim, self._bf16, w, "k_norm")
+        r = self._refs
+        st = self._call(self._c_append, r[0], r[1], r[2], layer, qp, qs, kp,
+                        ks, vp, vs, q_norm, k_norm, eps, rope, op, os_,
+                        self._st, self._stream(stream))
+        if st:
+            raise MpkError(st, "mpk_kv_append")
 
     def attend(self, layer: int, q, out, lse=None, scale: float = 0.0,
                stream=None):
         """mpk_prefix_attention of the new tokens over the cache."""
-        import torch
         w = "PagedBatch.attend"
-        self._layer(layer, w)
-        qp = self._rows(q, self.q_width, w, "q")
-        op = self._rows(out, self.q_width, w, "out")
-        lp = self._vec(lse, self.n_tokens * self.n_q_heads, torch.float32, w,
+        if not 0 <= layer < self.n_layers:
+            _refuse(w, f"layer {layer} of {self.n_layers}")
+        qp, qs = self._rows(q, self.q_width, w, "q")
+        op, os_ = self._rows(out, self.q_width, w, "out")
+        lp = self._vec(lse, self.n_tokens * self.n_q_heads, self._f32, w,
                        "lse")
+        r = self._refs
         if self._ws is None:
-            n = self._lib.mpk_prefix_attention_workspace(
-                self._refs[0], self._refs[1],
-                self._groups.n_groups if self._groups else 0)
+            import torch
+            n = self._c_attend_ws(r[0], r[1], self._groups.n_groups
+                                  if self._groups else 0)
             self._ws = torch.empty(max(n, 1), dtype=torch.uint8,
                                    device=self.device)
-        _check(self._call(
-            self._lib.mpk_prefix_attention, self._refs[0], self._refs[1],
-            self._refs[3], self._refs[2], layer, *qp, scale, *op, lp,
-            self._ws.data_ptr(), self._ws.numel(), self._st,
-            _stream_of(stream, self.device)), "mpk_prefix_attention")
+            self._ws_args = (self._ws.data_ptr(), self._ws.numel())
+        st = self._call(self._c_attend, r[0], r[1], r[3], r[2], layer, qp, qs,
+                        scale, op, os_, lp, *self._ws_args, self._st,
+                        self._stream(stream))
+        if st:
+            raise MpkError(st, "mpk_prefix_attention")
 
 
 class DraftVerifier(_OnDevice):
@@ -683,32 +702,32 @@ class DraftVerifier(_OnDevice):
         import torch
         w = "DraftVerifier"
         probe = torch.empty(0, dtype=torch.uint8, device=device)
-        self.device = _cuda_device(probe, w)
+        self._on(_cuda_device(probe, w))
         self.batch, self.n_tokens = batch, n_tokens
         self.vocab, self.max_out = vocab, max_out
-        self._lib = load_library()
-        self._tok = TokenBatch(batch, n_tokens, None, 0)
-        n = self._lib.mpk_verify_drafts_workspace(ctypes.byref(self._tok),
-                                                  vocab)
+        lib = load_library()
+        self._c_verify = lib.mpk_verify_drafts
+        self._tok = TokenBatch(batch, n_tokens, None,
+                               n_tokens // max(batch, 1))
+        n = lib.mpk_verify_drafts_workspace(ctypes.byref(self._tok), vocab)
         if n == 0 or not 1 <= max_out <= 128:
             raise MpkError(MPK_ERR_UNSUPPORTED if max_out > 128 else
                            MPK_ERR_INVALID_ARG, w)
         self._ws = torch.empty(n, dtype=torch.uint8, device=self.device)
         self._status = status
         self._st = self._vec(status, 1, torch.int32, w, "status")
-        self._args = VerifyArgs()
+        self._args = VerifyArgs(vocab=vocab, max_out=max_out)
+        self._refs = (ctypes.byref(self._tok), ctypes.byref(self._args))
+        self._ws_args = (self._ws.data_ptr(), n)
 
     def _matrix(self, t, rows, where, name):
-        import torch
-        if t is None:
-            return None, 0
-        if (t.dtype is not torch.float32 or t.device != self.device or
-                t.dim() != 2 or t.shape[0] < rows or
-                t.shape[1] != self.vocab or
-                (self.vocab > 1 and t.stride(1) != 1)):
+        sh, st = t.shape, t.stride()
+        if (t.dtype is not self._f32 or t.get_device() != self._index or
+                len(sh) != 2 or sh[0] < rows or sh[1] != self.vocab or
+                (self.vocab > 1 and st[1] != 1)):
             _refuse(where, f"{name} must be float32 [{rows}, {self.vocab}] on "
                            f"{self.device} with contiguous rows")
-        return t.data_ptr(), (t.stride(0) if rows > 1 else self.vocab)
+        return t.data_ptr(), (st[0] if rows > 1 else self.vocab)
 
     def verify(self, tokens, logits, uniform, noise, n_accepted, out_tokens,
                q_start=None, draft=None, draft_is_logits: bool = False,
@@ -716,34 +735,35 @@ class DraftVerifier(_OnDevice):
                seq_lens=None, seq_lens_out=None, stream=None):
         """Accept or refuse the drafts and sample the next tokens; arguments
         and outputs as in include/mpk.h (mpk_verify_args)."""
-        import torch
         w = "DraftVerifier.verify"
-        B, n, i32, f32 = self.batch, self.n_tokens, torch.int32, torch.float32
-        self._tok.q_start = self._vec(q_start, B + 1, i32, w, "q_start")
-        if q_start is None and n % B:
-            _refuse(w, "n_tokens must be a multiple of the batch without "
-                       "q_start")
-        self._tok.tokens_per_seq = n // B
-        lg = self._matrix(logits, n, w, "logits")
-        dr = self._matrix(draft, n, w, "draft")
-        no = self._matrix(noise, B, w, "noise")
+        B, n, i32, f32, vec = (self.batch, self.n_tokens, self._i32,
+                               self._f32, self._vec)
+        if q_start is None:
+            if n % B:
+                _refuse(w, "n_tokens must be a multiple of the batch without "
+                           "q_start")
+            self._tok.q_start = None
+        else:
+            self._tok.q_start = vec(q_start, B + 1, i32, w, "q_start")
         bo = B * self.max_out
         a = self._args
-        a.vocab, a.max_out = self.vocab, self.max_out
-        a.tokens = self._vec(tokens, n, i32, w, "tokens")
-        a.logits, a.logits_stride = lg
-        a.draft, a.draft_stride = dr
-        a.draft_is_logits = int(bool(draft_is_logits))
-        a.temperature = self._vec(temperature, B, f32, w, "temperature")
-        a.uniform = self._vec(uniform, n, f32, w, "uniform")
-        a.noise, a.noise_stride = no
-        a.n_accepted = self._vec(n_accepted, B, i32, w, "n_accepted")
-        a.out_tokens = self._vec(out_tokens, bo, i32, w, "out_tokens")
-        a.logprobs = self._vec(logprobs, bo, f32, w, "logprobs")
-        a.next_tokens = self._vec(next_tokens, B, i32, w, "next_tokens")
-        a.seq_lens = self._vec(seq_lens, B, i32, w, "seq_lens")
-        a.seq_lens_out = self._vec(seq_lens_out, B, i32, w, "seq_lens_out")
-        _check(self._call(
-            self._lib.mpk_verify_drafts, ctypes.byref(self._tok),
-            ctypes.byref(a), self._ws.data_ptr(), self._ws.numel(), self._st,
-            _stream_of(stream, self.device)), "mpk_verify_drafts")
+        a.tokens = vec(tokens, n, i32, w, "tokens")
+        a.logits, a.logits_stride = self._matrix(logits, n, w, "logits")
+        if draft is None:
+            a.draft = None
+        else:
+            a.draft, a.draft_stride = self._matrix(draft, n, w, "draft")
+            a.draft_is_logits = 1 if draft_is_logits else 0
+        a.temperature = vec(temperature, B, f32, w, "temperature")
+        a.uniform = vec(uniform, n, f32, w, "uniform")
+        a.noise, a.noise_stride = self._matrix(noise, B, w, "noise")
+        a.n_accepted = vec(n_accepted, B, i32, w, "n_accepted")
+        a.out_tokens = vec(out_tokens, bo, i32, w, "out_tokens")
+        a.logprobs = vec(logprobs, bo, f32, w, "logprobs")
+        a.next_tokens = vec(next_tokens, B, i32, w, "next_tokens")
+        a.seq_lens = vec(seq_lens, B, i32, w, "seq_lens")
+        a.seq_lens_out = vec(seq_lens_out, B, i32, w, "seq_lens_out")
+        st = self._call(self._c_verify, *self._refs, *self._ws_args,
+                        self._st, self._stream(stream))
+        if st:
+            raise MpkError(st, "mpk_verify_drafts")
