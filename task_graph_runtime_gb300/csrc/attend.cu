@@ -19,16 +19,17 @@ struct Found {
   int64_t at;          // row 0's index into ml (in rows) of the first slot
   int n;
 };
-__device__ __forceinline__ Found find(const AttnSet& s, int e, int row, int Hkv,
-                                      int h) {
-  const int r = row % s.M;
-  const int64_t unit = ((int64_t)s.ebase[e] + row / s.M) * Hkv + h;
+__device__ __forceinline__ Found find(const AttendArgs& a, const AttnSet& s,
+                                      int tok0, int e, int row, int h) {
   Found f{0, 0};
-  if (row < 0 || unit < 0 || unit >= s.units) return f;
-  const int2 me = s.meta[unit];
+  if (row < 0) return f;
+  const int tile = row / s.M;
+  const int64_t at = meta_of(a.p, tok0, e, tile, s.M, h);
+  if (at >= s.units) return f;
+  const int2 me = s.meta[at];
   // (only arrays that are not ascending leave anything else here)
   if (me.x < 0 || me.y < 0 || me.y > s.slots - me.x) return f;
-  f.at = (int64_t)me.x * s.M + r;
+  f.at = (int64_t)me.x * s.M + (row - tile * s.M);
   f.n = me.y;
   return f;
 }
@@ -56,9 +57,9 @@ __global__ void __launch_bounds__(kNT)
   sv_grid_wait();
   Found fp{0, 0}, fo{0, 0};
   if (pre.k1 > 0)
-    fp = find(a.pre, g, (t - pre.tok0) * grp + j, p.Hkv, h);
+    fp = find(a, a.pre, pre.tok0, g, (t - pre.tok0) * grp + j, h);
   if (own.k1 > own.k0)
-    fo = find(a.own, b, (t - own.tok0) * grp + j, p.Hkv, h);
+    fo = find(a, a.own, own.tok0, b, (t - own.tok0) * grp + j, h);
   const int n = fp.n + fo.n;
   float m = -INFINITY, l = 0.f, acc[V];
 #pragma unroll
@@ -201,17 +202,18 @@ size_t attend_workspace(AttendArgs* a, char* base) {
   const int64_t per = (rows + a->p.batch - 1) / a->p.batch;
   const int64_t all = a->n_groups ? (rows + a->n_groups - 1) / a->n_groups : 0;
   // the smallest row tiles that hold them; few pairs are built
-  a->wmo = per <= 16 ? 1 : per <= 32 ? 2 : 4;
+  a->wmo = per <= 8 ? 0 : per <= 16 ? 1 : per <= 32 ? 2 : 4;
   a->box = attend_box(a->p);
   a->tc = all > 64 && a->box && a->p.d >= 64 && a->scale_log2 > 0.f;
-  a->wmp = a->wmo > 1 || (all > 16 && !a->tc) ? 4 : 1;
-  a->own.M = 16 * a->wmo;
-  a->pre.M = a->tc ? attend_tc_rows() : 16 * a->wmp;
+  a->wmp = !a->n_groups || a->tc || all <= (a->wmo ? 16 * a->wmo : 8)
+               ? a->wmo
+               : 4;
+  a->own.M = a->wmo ? 16 * a->wmo : 8;
+  a->pre.M = a->tc ? attend_tc_rows() : a->wmp ? 16 * a->wmp : 8;
   // a set holds the results of n entities whose rows are disjoint
   auto place = [&](AttnSet* s, int64_t n, int ctas) {
     s->units = (rows / s->M + n) * a->p.Hkv;
     s->slots = s->units + ctas;
-    s->ebase = reinterpret_cast<int32_t*>(take(n * 4));
     s->meta = reinterpret_cast<int2*>(take(s->units * 8));
     s->ml = reinterpret_cast<float2*>(take(s->slots * s->M * 8));
     s->part = reinterpret_cast<float*>(

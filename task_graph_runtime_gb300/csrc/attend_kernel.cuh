@@ -15,6 +15,10 @@
 // of 64; mma.sync m16n8k16, scores and weights stay in registers.  With few
 // rows the warps split the keys, so that the tensor instructions per block
 // stay few; the kernel is bound by the K/V bytes.
+// WM = 0 is a tile of 8 rows, one token's heads as a rule: the products are
+// turned over (S^T = K Q^T, O^T = V^T P^T) so that the keys fill the 16 rows
+// of the instruction and the queries its 8 columns.  That is half the tensor
+// instructions, half the registers, and three or four CTAs an SM.
 // A fifth warp walks the stretch ahead of them: it looks up the pages (one
 // block early), copies K, V and the queries of a 16-row tile into a ring of
 // kStages shared-memory stages, and leaves a description of the block there.
@@ -75,6 +79,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4],
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The 8 x 8 matrix of 16-bit values that the warp holds, turned over.
+__device__ __forceinline__ uint32_t turn8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 // 2^x, exact 0 for -inf
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -103,12 +113,18 @@ struct Blk {
 };
 enum { BLK_PREFIX = 1, BLK_FIRST = 2, BLK_LAST = 4, BLK_STOP = 8 };
 
-template <int D>
+__host__ __device__ constexpr int tile_rows(int wm) {
+  return wm ? 16 * wm : 8;
+}
+
+// FEW: 8-row tiles alone.
+template <int D, bool FEW = false>
 struct Cfg {
-  // CTAs an SM and stages a CTA: the consumers' registers allow two or three
-  // CTAs; the stages fill the shared memory that they share.
-  static constexpr int kCtas = D == 128 ? 2 : 3;
-  static constexpr int kStages = D == 128 ? 3 : 4;
+  // CTAs an SM and stages a CTA: what the consumers' registers allow; the
+  // stages fill the shared memory that they share.
+  static constexpr int kCtas = FEW ? (D == 128 ? 3 : 4) : (D == 128 ? 2 : 3);
+  static constexpr int kStages =
+      FEW ? (D == 128 ? 2 : D == 64 ? 3 : 4) : (D == 128 ? 3 : 4);
   static constexpr int kTile = kBN * D * 2;            // bytes of K (or V)
   static constexpr int kQ = 16 * D * 2;                // queries of 16 rows
   // (stages on 1024 bytes: the period of the swizzle)
@@ -132,7 +148,7 @@ struct Cursor {
 // The copying warp.
 template <int D, int WMP, int WMO>
 struct Copier {
-  using C = Cfg<D>;
+  using C = Cfg<D, WMP == 0>;
   static constexpr int CH = C::CH;
   const AttendArgs& a;
   uint8_t* smem;
@@ -145,7 +161,7 @@ struct Copier {
     return i < G ? att_group_ent(a, i) : att_seq_ent(a, i - G);
   }
   __device__ __forceinline__ void enter(Cursor& c) const {
-    const int M = c.e < G ? 16 * WMP : 16 * WMO;
+    const int M = c.e < G ? tile_rows(WMP) : tile_rows(WMO);
     c.E = ent(c.e);
     c.nb = blocks_of<kBN>(c.E);
     c.units = c.nb > 0 ? ((c.E.rows + M - 1) / M) * a.p.Hkv : 0;
@@ -225,9 +241,11 @@ struct Copier {
                 (last ? BLK_LAST : 0) | (stop ? BLK_STOP : 0);
       if (lane == 0 && c.blk == 0 && !stop) {
         const int end = plan_owner(x + c.nb - 1, ps.total, ps.n);
-        set.meta[d.unit] =
-            make_int2(d.unit + (int)blockIdx.x, end - (int)blockIdx.x + 1);
-        if (c.u == 0) set.ebase[prefix ? c.e : c.e - G] = c.unit0 / p.Hkv;
+        const int64_t at = meta_of(p, d.tok0, prefix ? c.e : c.e - G, d.tile,
+                                   tile_rows(wm), d.h);
+        if (at < set.units)
+          set.meta[at] =
+              make_int2(d.unit + (int)blockIdx.x, end - (int)blockIdx.x + 1);
       }
       // rows of the pool (32-bit numbers: 2^32 rows of 64 bytes are more
       // than the memory)
@@ -246,10 +264,11 @@ struct Copier {
       if (c.left > 0) pages(c, pg);
       if (!bar_wait(empty + 8 * st, ph, dead)) break;
       const uint32_t ks = t_addr(smem + st * C::kStage);
-      if (first && wm == 1 && !stop) {
+      if (first && wm <= 1 && !stop) {
 #pragma unroll
         for (int i = 0; i < 16 / RW; ++i) {
-          const int r = r0 + i * RW, rw = d.tile * 16 + r;
+          const int r = r0 + i * RW, rw = d.tile * tile_rows(wm) + r;
+          if (wm == 0 && r >= 8) break;
           const bool ok = rw < d.rows;
           const int tok = ok ? rw / grp : 0;
           cp16(ks + 2 * C::kTile + swz<D, 16>(r, ch),
@@ -329,15 +348,17 @@ struct Seg {
 };
 
 // The warps that compute.
-template <int D>
+template <int D, bool FEW>
 struct Attend {
-  using C = Cfg<D>;
+  using C = Cfg<D, FEW>;
   static constexpr int CH = C::CH;
 
   const AttendArgs& a;
   uint8_t* smem;
   float (*s_ml)[2];    // [4 * 16] of each warp's rows
 
+  // (a tile of 8 rows uses two words of each of qf and half of o, and its
+  // thread's rows are 2 (lane % 4) and the next)
   uint32_t qf[D / 16][4];
   float o[D / 8][4];
   float m[2], l[2];
@@ -347,15 +368,26 @@ struct Attend {
   // stage, or for a larger tile from memory.
   template <int WM>
   __device__ __forceinline__ void queries(const Blk& b, int st) {
-    const int lane = threadIdx.x & 31, wm = (threadIdx.x >> 5) % WM;
-    if constexpr (WM == 1) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (WM == 0) {
+      const uint32_t q = t_addr(smem + st * C::kStage + 2 * C::kTile);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t b[4];
+        ldm4(q + swz<D, 16>(lane & 7, 4 * k + (lane >> 3)), b);
+        qf[2 * k][0] = b[0];
+        qf[2 * k][1] = b[1];
+        qf[2 * k + 1][0] = b[2];
+        qf[2 * k + 1][1] = b[3];
+      }
+    } else if constexpr (WM == 1) {
       const uint32_t q = t_addr(smem + st * C::kStage + 2 * C::kTile);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
         ldm4(q + swz<D, 16>(lane & 15, 2 * k + (lane >> 4)), qf[k]);
-      return;
-    }
+    } else {
     const PagedArgs& p = a.p;
+    const int wm = (threadIdx.x >> 5) % WM;
     const int grp = p.Hq / p.Hkv;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -375,6 +407,7 @@ struct Attend {
                : 0u;
       }
     }
+    }
   }
 
   template <int WM>
@@ -389,19 +422,95 @@ struct Attend {
     } else {
       // the last token's rows see all of k1; each token before one fewer
       const int grp = a.p.Hq / a.p.Hkv, n = b.rows / grp;
-      const int r0 = b.tile * 16 * WM;
-      const int lane = threadIdx.x & 31, wm = (threadIdx.x >> 5) % WM;
+      const int r0 = b.tile * tile_rows(WM);
+      const int lane = threadIdx.x & 31;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        s.lim[i] = s.k1 - (n - 1) +
-                   min((r0 + wm * 16 + (lane >> 2) + 8 * i) / grp, n - 1);
+      for (int i = 0; i < 2; ++i) {
+        const int r = WM == 0 ? 2 * (lane & 3) + i
+                              : (threadIdx.x >> 5) % (WM ? WM : 1) * 16 +
+                                    (lane >> 2) + 8 * i;
+        s.lim[i] = s.k1 - (n - 1) + min((r0 + r) / grp, n - 1);
+      }
       s.lim_min = s.k1 - (n - 1) + min(r0 / grp, n - 1);
     }
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (int i = 0; i < (WM == 0 ? D / 16 : D / 8); ++i)
+      o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
     return s;
+  }
+
+  // The same for a tile of 8 rows; a warp has 16 keys.
+  __device__ __forceinline__ void block8(const Seg& sg, int kb, int st) {
+    const int lane = threadIdx.x & 31, wn = threadIdx.x >> 5;
+    uint8_t* kt = smem + st * C::kStage;
+    uint8_t* vt = kt + C::kTile;
+    // ---- scores: s[2 i + r] is key lane / 4 + 8 i, row 2 (lane % 4) + r
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < D / 16; k += 2) {
+      uint32_t b[4];
+      ldm4(t_addr(kt) + swz<D, kBN>(wn * 16 + (lane & 15), 2 * k + (lane >> 4)),
+           b);
+      mma16816(s, b, qf[k][0], qf[k][1]);
+      ldm4(t_addr(kt) +
+               swz<D, kBN>(wn * 16 + (lane & 15), 2 * k + 2 + (lane >> 4)),
+           b);
+      mma16816(s2, b, qf[k + 1][0], qf[k + 1][1]);
+    }
+    const bool masked = kb + kBN > sg.lim_min || kb < sg.k0;
+    const int key0 = kb + wn * 16 + (lane >> 2);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      s[q] = (s[q] + s2[q]) * a.scale_log2;
+      const int key = key0 + 8 * (q >> 1);
+      if (masked && (key >= sg.lim[q & 1] || key < sg.k0)) s[q] = -INFINITY;
+    }
+    // ---- running maximum and sum, as in block()
+    float top[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 4));
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 8));
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 16));
+    }
+    if (__any_sync(0xffffffffu,
+                   top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
+      float f[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float mn = fmaxf(m[r], top[r]);
+        f[r] = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
+        m[r] = mn;
+        l[r] *= f[r];
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[i][q] *= f[q & 1];
+    }
+    float w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      w[q] = ex2(s[q] - (m[q & 1] == -INFINITY ? 0.f : m[q & 1]));
+    l[0] += w[0] + w[2];
+    l[1] += w[1] + w[3];
+    const uint32_t p0 = sv_pack(w[0], w[1]), p1 = sv_pack(w[2], w[3]);
+    if (a.box && (kb < sg.k0 || kb + kBN > sg.k1))
+      clear_values<0>(vt, sg.k0 - kb, sg.k1 - kb, wn);
+    if (masked && !sg.prefix && sg.lim_min < sg.k1)
+      fix_values8(vt, kb, wn, sg.lim, p0, p1);
+    // ---- weighted values: rows and keys of the weights change places
+    const uint32_t b0 = turn8(p0), b1 = turn8(p1);
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) {
+      uint32_t b[4];
+      ldm4t(t_addr(vt) + swz<D, kBN>(wn * 16 + (lane & 7) + ((lane >> 4) << 3),
+                                     2 * n + ((lane >> 3) & 1)),
+            b);
+      mma16816(o[n], b, b0, b1);
+    }
   }
 
   template <int WM>
@@ -516,14 +625,26 @@ struct Attend {
   template <int WM>
   __device__ __forceinline__ void finish(const AttnSet& set, int64_t slot,
                                          int valid, int st) {
-    constexpr int WN = 4 / WM, M = 16 * WM;
+    constexpr int WN = WM ? 4 / (WM ? WM : 1) : 4, M = tile_rows(WM);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int wm = warp % WM, wn = warp / WM;
+    const int wm = WM ? warp % (WM ? WM : 1) : 0;
+    const int wn = WM ? warp / (WM ? WM : 1) : warp;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if (WM) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      } else {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 4);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 8);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 16);
+      }
     }
+    // row of value r of m, l and (by halves) o, and the lanes that speak for it
+    auto row_of = [&](int r) {
+      return WM ? wm * 16 + (lane >> 2) + 8 * r : 2 * (lane & 3) + r;
+    };
+    const bool speaks = WM ? (lane & 3) == 0 : lane < 4;
     float* part = set.part + slot * M * D;
     float2* ml = set.ml + slot * M;
     if constexpr (WN == 1) {
@@ -540,10 +661,10 @@ struct Attend {
       }
     } else {
       // ---- join the WN warps that share these rows
-      if ((lane & 3) == 0)
+      if (speaks)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int row = wm * 16 + (lane >> 2) + 8 * r;
+          const int row = row_of(r);
           s_ml[wn * M + row][0] = m[r];
           s_ml[wn * M + row][1] = l[r];
         }
@@ -552,7 +673,7 @@ struct Attend {
       float f[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int row = wm * 16 + (lane >> 2) + 8 * r;
+        const int row = row_of(r);
         float top = -INFINITY;
 #pragma unroll
         for (int w = 0; w < WN; ++w) top = fmaxf(top, s_ml[w * M + row][0]);
@@ -574,9 +695,17 @@ struct Attend {
       for (int r0 = 0; r0 < M; r0 += C::kPass) {
         if (r0 >= valid) break;
         if (r0 > 0) sync_threads(1, kComp);
+        if (WM == 0) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              buf[(wn * C::kPass + 2 * (lane & 3) + (q & 1)) * C::kPitch +
+                  i * 16 + (lane >> 2) + 8 * (q >> 1)] = o[i][q] * f[q & 1];
+        }
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          if (wm * 16 + 8 * r == r0) {
+          if (WM > 0 && wm * 16 + 8 * r == r0) {
             const int row = lane >> 2;
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
@@ -610,9 +739,9 @@ struct Attend {
   template <int WM>
   __device__ __forceinline__ void clear_values(uint8_t* vt, int lo, int hi,
                                                int wn) {
-    constexpr int NK = 16 * WM;
-    const int lane = threadIdx.x & 31, wm = (threadIdx.x >> 5) % WM;
-    for (int i = wm * 32 + lane; i < NK * CH; i += 32 * WM) {
+    constexpr int W = WM ? WM : 1, NK = 16 * W;
+    const int lane = threadIdx.x & 31, wm = (threadIdx.x >> 5) % W;
+    for (int i = wm * 32 + lane; i < NK * CH; i += 32 * W) {
       const int r = wn * NK + i / CH;
       if (r < lo || r >= hi)
         *reinterpret_cast<uint4*>(vt + swz<D, kBN>(r, i % CH)) =
@@ -632,20 +761,7 @@ struct Attend {
     constexpr int NK = 16 * WM;
     const int lane = threadIdx.x & 31;
     uint32_t bad[2] = {0, 0};    // keys of the slice with such a value
-    for (int i = lane; i < NK * CH; i += 32) {
-      const int k = i / CH;
-      const uint4 u =
-          *reinterpret_cast<const uint4*>(vt + swz<D, kBN>(wn * NK + k, i % CH));
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-      bool b = false;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        b |= (w[q] & 0x7f80u) == 0x7f80u ||
-             (w[q] & 0x7f800000u) == 0x7f800000u;
-      if (b) bad[k >> 5] |= 1u << (k & 31);
-    }
-    bad[0] = __reduce_or_sync(0xffffffffu, bad[0]);
-    bad[1] = __reduce_or_sync(0xffffffffu, bad[1]);
+    find_bad<NK>(vt, wn, bad);
     if (!(bad[0] | bad[1])) return;
     for (int k = 0; k < NK; ++k) {
       const int r = wn * NK + k;
@@ -676,7 +792,63 @@ struct Attend {
     }
     if (WM > 1) sync_threads(2 + wn, 32 * WM);
     else __syncwarp();
-    for (int i = lane; i < NK * CH; i += 32) {
+    drop_bad<NK>(vt, wn);
+    if (WM > 1) sync_threads(2 + wn, 32 * WM);
+    else __syncwarp();
+    fence_async();
+  }
+  // Tile of 8 rows: p0, p1 hold the weights of keys lane / 4 and + 8.
+  __device__ __forceinline__ void fix_values8(uint8_t* vt, int kb, int wn,
+                                              const int (&lim)[2], uint32_t p0,
+                                              uint32_t p1) {
+    const int lane = threadIdx.x & 31;
+    uint32_t bad[2] = {0, 0};
+    find_bad<16>(vt, wn, bad);
+    if (!bad[0]) return;
+    for (int k = 0; k < 16; ++k) {
+      const int r = wn * 16 + k;
+      if (!((bad[0] >> k) & 1u)) continue;
+      const uint32_t w = __shfl_sync(0xffffffffu, k < 8 ? p0 : p1,
+                                     ((k & 7) << 2) | (lane & 3));
+      const float p[2] = {sv_lo(w), sv_hi(w)};
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = i * 16 + (lane >> 2) + 8 * (q >> 1);
+          const float v = sv_lo(*reinterpret_cast<const uint16_t*>(
+              vt + swz<D, kBN>(r, c / 8) + 2 * (c % 8)));
+          if (!isfinite(v) && kb + r < lim[q & 1]) o[i][q] += p[q & 1] * v;
+        }
+    }
+    __syncwarp();
+    drop_bad<16>(vt, wn);
+    __syncwarp();
+    fence_async();
+  }
+  // Keys of slice wn with a value that is not finite.
+  template <int NK>
+  __device__ __forceinline__ void find_bad(const uint8_t* vt, int wn,
+                                           uint32_t (&bad)[2]) {
+    for (int i = threadIdx.x & 31; i < NK * CH; i += 32) {
+      const int k = i / CH;
+      const uint4 u = *reinterpret_cast<const uint4*>(
+          vt + swz<D, kBN>(wn * NK + k, i % CH));
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      bool b = false;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        b |= (w[q] & 0x7f80u) == 0x7f80u ||
+             (w[q] & 0x7f800000u) == 0x7f800000u;
+      if (b) bad[k >> 5] |= 1u << (k & 31);
+    }
+    bad[0] = __reduce_or_sync(0xffffffffu, bad[0]);
+    bad[1] = __reduce_or_sync(0xffffffffu, bad[1]);
+  }
+  // Zeros in their places.
+  template <int NK>
+  __device__ __forceinline__ void drop_bad(uint8_t* vt, int wn) {
+    for (int i = threadIdx.x & 31; i < NK * CH; i += 32) {
       uint32_t* w = reinterpret_cast<uint32_t*>(
           vt + swz<D, kBN>(wn * NK + i / CH, i % CH));
 #pragma unroll
@@ -687,9 +859,17 @@ struct Attend {
         w[q] = u;
       }
     }
-    if (WM > 1) sync_threads(2 + wn, 32 * WM);
-    else __syncwarp();
-    fence_async();
+  }
+
+  template <int WM>
+  __device__ __forceinline__ void step(Seg& sg, const Blk& b,
+                                       const AttnSet& set, int64_t slot,
+                                       int st) {
+    if (b.flags & BLK_FIRST) sg = begin<WM>(b, st);
+    if constexpr (WM == 0) block8(sg, b.key, st);
+    else block<WM>(sg, b.key, st);
+    if (b.flags & BLK_LAST)
+      finish<WM>(set, slot, b.rows - b.tile * tile_rows(WM), st);
   }
 
   // The whole stretch of n blocks.
@@ -708,15 +888,9 @@ struct Attend {
       const AttnSet& set = prefix ? a.pre : a.own;
       const int64_t slot = (int64_t)b.unit + blockIdx.x;
       if (WMP != WMO && prefix) {
-        if (b.flags & BLK_FIRST) sg = begin<WMP>(b, st);
-        block<WMP>(sg, b.key, st);
-        if (b.flags & BLK_LAST)
-          finish<WMP>(set, slot, b.rows - b.tile * 16 * WMP, st);
+        if constexpr (WMP != WMO) step<WMP>(sg, b, set, slot, st);
       } else {
-        if (b.flags & BLK_FIRST) sg = begin<WMO>(b, st);
-        block<WMO>(sg, b.key, st);
-        if (b.flags & BLK_LAST)
-          finish<WMO>(set, slot, b.rows - b.tile * 16 * WMO, st);
+        step<WMO>(sg, b, set, slot, st);
       }
       __syncwarp();
       if ((threadIdx.x & 31) == 0) bar_arrive(empty + 8 * st);
@@ -729,11 +903,11 @@ struct Attend {
 };
 
 template <int D, int WMP, int WMO>
-__global__ void __launch_bounds__(kNT, WMP > 1 ? 2 : Cfg<D>::kCtas)
+__global__ void __launch_bounds__(kNT, WMP > 1 ? 2 : Cfg<D, WMP == 0>::kCtas)
     attend_kernel(const __grid_constant__ AttendArgs a) {
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = raw + (1024 - (t_addr(raw) & 1023)) % 1024;
-  constexpr int kStages = Cfg<D>::kStages;
+  constexpr int kStages = Cfg<D, WMP == 0>::kStages;
   __shared__ float s_ml[64][2];
   __shared__ Blk s_blk[kStages];
   __shared__ __align__(8) uint64_t bars[2 * kStages];
@@ -756,14 +930,14 @@ __global__ void __launch_bounds__(kNT, WMP > 1 ? 2 : Cfg<D>::kCtas)
                          empty, &s_dead, a.tc ? 0 : a.n_groups, 0};
   cp.n_ent = cp.G + a.p.batch;
   // (its barriers also publish the initialisation above)
-  const PlanStart ps = plan_start<kNT, 16 * WMP, 16 * WMO, kBN>(
+  const PlanStart ps = plan_start<kNT, tile_rows(WMP), tile_rows(WMO), kBN>(
       cp.G, cp.n_ent, a.p.Hkv, [&](int i) { return cp.ent(i); }, blockIdx.x,
       gridDim.x);
   if (ps.x0 < ps.x1) {
     if (threadIdx.x >= kComp) {
       cp.run(ps);
     } else {
-      Attend<D> t{a, smem, s_ml};
+      Attend<D, WMP == 0> t{a, smem, s_ml};
       t.template run<WMP, WMO>(s_blk, full, empty, &s_dead, ps.x1 - ps.x0);
     }
     __syncthreads();
@@ -774,20 +948,23 @@ __global__ void __launch_bounds__(kNT, WMP > 1 ? 2 : Cfg<D>::kCtas)
 
 template <int D, int WMP, int WMO>
 cudaError_t run_tiles(const AttendArgs& a, cudaStream_t s) {
+  using C = Cfg<D, WMP == 0>;
   auto k = attend_kernel<D, WMP, WMO>;
   cudaError_t e = cudaFuncSetAttribute(
-      k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+      k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  const int ctas = WMP > 1 ? 2 : Cfg<D>::kCtas;
-  return sv_launch(k, dim3(attend_ctas() / 4 * ctas), kNT, Cfg<D>::kSmem, s, a);
+  const int ctas = WMP > 1 ? 2 : C::kCtas;
+  return sv_launch(k, dim3(attend_ctas() / 4 * ctas), kNT, C::kSmem, s, a);
 }
 
 template <int D>
 cudaError_t run_attend(const AttendArgs& a, cudaStream_t s) {
   if (a.wmo == 4) return run_tiles<D, 4, 4>(a, s);
   if (a.wmo == 2) return run_tiles<D, 4, 2>(a, s);
-  if (a.wmp == 4) return run_tiles<D, 4, 1>(a, s);
-  return run_tiles<D, 1, 1>(a, s);
+  if (a.wmo == 1 && a.wmp == 4) return run_tiles<D, 4, 1>(a, s);
+  if (a.wmo == 1) return run_tiles<D, 1, 1>(a, s);
+  if (a.wmp == 4) return run_tiles<D, 4, 0>(a, s);
+  return run_tiles<D, 0, 0>(a, s);
 }
 
 }  // namespace

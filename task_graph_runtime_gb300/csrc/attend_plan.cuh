@@ -153,6 +153,15 @@ __device__ __forceinline__ int blocks_of(const Ent& e) {
   return e.k1 > e.k0 ? (e.k1 + BN - 1) / BN - e.k0 / BN : 0;
 }
 
+// Where the segments of a unit are noted: a number that a row gives without
+// looking anything up.  Tiles of entity e (of its kind) begin at row
+// tok0 * heads of all rows; the entities' tiles do not meet because each
+// entity adds one to the quotient.  Below rows / M + entities.
+__device__ __forceinline__ int64_t meta_of(const PagedArgs& p, int tok0, int e,
+                                           int tile, int M, int h) {
+  return ((int64_t)tok0 * (p.Hq / p.Hkv) / M + e + tile) * p.Hkv + h;
+}
+
 // Where a CTA starts on the line.
 struct PlanStart {
   int64_t x0, x1;      // this CTA's stretch

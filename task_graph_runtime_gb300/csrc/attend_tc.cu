@@ -47,21 +47,32 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
       "[%0];" ::"r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b,
+// Shared-memory operands: 128-byte swizzled rows in 8-row groups 1024 bytes
+// apart.  The upper word of the descriptor says that; the lower one has the
+// address, and for an operand whose rows run along the product's inner
+// dimension the distance of its 64-value column panels.
+constexpr uint32_t kOperandHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t panel) {
+  return ((addr & 0x3ffff) >> 4) | ((panel >> 4) << 16);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b,
                                        uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "r"(kOperandHi)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b,
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b,
                                        uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(
           d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "r"(kOperandHi)
       : "memory");
 }
 __device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t* r) {
@@ -79,18 +90,30 @@ __device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t* r) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t* r) {
+__device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
+        "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
       "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
-      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31])
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 __device__ __forceinline__ void tm_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
@@ -104,15 +127,6 @@ __device__ __forceinline__ float ex2t(float x) {
   return y;
 }
 
-// Shared-memory operand descriptor: 128-byte swizzled rows (8-row groups of
-// 1024 bytes), groups `stride` bytes apart; `lead` separates the 64-value
-// column panels of an operand whose rows run along the product's inner
-// dimension.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead,
-                                            uint32_t stride) {
-  return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(lead >> 4) << 16) |
-         ((uint64_t)(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
 // bf16 x bf16 to fp32, M = 128
 __device__ constexpr uint32_t product(int n, bool b_columns) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_columns ? 1u : 0u) << 16) |
@@ -193,34 +207,42 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   // All roles walk the same segments.  f(E, tile, h, blk, n, slot, two):
   // `two`: the tile has rows in its second slot.  f returns false to stop.
   auto walk = [&](bool writes_meta, auto f) {
-    int64_t x = st.x0, off = st.off, unit0 = st.unit0;
-    for (int e = st.e; x < st.x1 && e < a.n_groups; ++e, off = 0) {
-      const Ent E = att_group_ent(a, e);
-      const int nb = (E.k1 - E.k0 + kKeys - 1) / kKeys;
-      const int64_t units =
-          nb > 0 ? (int64_t)((E.rows + kRows - 1) / kRows) * Hkv : 0;
-      while (x < st.x1 && off < units * nb) {
-        const int u = (int)(off / nb), blk = (int)(off - (int64_t)u * nb);
-        const int n = (int)min((int64_t)(nb - blk), st.x1 - x);
-        const int64_t unit = unit0 + u;
-        if (unit >= a.pre.units) {   // q_start or group_start not ascending
-          sv_latch(p.status, MPK_ERR_INVALID_ARG);
-          return;
-        }
-        if (writes_meta && blk == 0) {
-          const int last = plan_owner(x + nb - 1, st.total, st.n);
-          a.pre.meta[unit] =
-              make_int2((int)(unit + blockIdx.x), last - (int)blockIdx.x + 1);
-          if (u == 0) a.pre.ebase[e] = (int)(unit0 / Hkv);
-        }
-        const int tile = u / Hkv;
-        if (!f(E, tile, u % Hkv, blk, n, unit + blockIdx.x,
-               E.rows > tile * kRows + 128))
-          return;
-        x += n;
-        off += n;
+    int64_t left = st.x1 - st.x0;
+    if (left <= 0) return;
+    int e = st.e, unit0 = st.unit0;
+    Ent E = att_group_ent(a, e);
+    int nb = blocks_of<kKeys>(E);
+    int u = (int)(st.off / nb), blk = (int)(st.off - (int64_t)u * nb);
+    while (true) {
+      const int unit = unit0 + u, tile = u / Hkv;
+      const int n = (int)min((int64_t)(nb - blk), left);
+      if (unit >= a.pre.units) {   // q_start or group_start not ascending
+        sv_latch(p.status, MPK_ERR_INVALID_ARG);
+        return;
       }
-      unit0 += units;
+      if (writes_meta && blk == 0) {
+        const int last = plan_owner(st.x1 - left + nb - 1, st.total, st.n);
+        const int64_t at = meta_of(p, E.tok0, e, tile, kRows, u - tile * Hkv);
+        if (at < a.pre.units)
+          a.pre.meta[at] =
+              make_int2(unit + (int)blockIdx.x, last - (int)blockIdx.x + 1);
+      }
+      if (!f(E, tile, u - tile * Hkv, blk, n, unit + (int)blockIdx.x,
+             E.rows > tile * kRows + 128))
+        return;
+      left -= n;
+      if (left <= 0) return;
+      blk = 0;
+      ++u;
+      int units = (E.rows + kRows - 1) / kRows * Hkv;
+      while (u >= units) {
+        unit0 += units;
+        if (++e >= a.n_groups) return;
+        E = att_group_ent(a, e);
+        nb = blocks_of<kKeys>(E);
+        units = nb > 0 ? (E.rows + kRows - 1) / kRows * Hkv : 0;
+        u = 0;
+      }
     }
   };
 
@@ -231,7 +253,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     // ---------------------------------------------------------- loads
     int it = 0, sent[2] = {0, 0};
     uint32_t tail_ph = 0;
-    walk(lane == 0, [&](const Ent& E, int, int h, int blk, int n, int64_t,
+    walk(lane == 0, [&](const Ent& E, int, int h, int blk, int n, int,
                         bool) {
       const int32_t* pt = p.page_table + (int64_t)E.seq * p.max_pages;
       for (int j = 0; j < n; ++j, ++it) {
@@ -308,20 +330,22 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     constexpr uint32_t iqk = product(kKeys, false), ipv = product(D, true);
     int it = 0;
     uint32_t pn[2] = {0, 0}, qn[2] = {0, 0};
+    const uint32_t dq = operand(base + L::kQ, 16),
+                   dk = operand(base + L::kK, 16),
+                   dv = operand(base + L::kV, L::kPanel);
+    constexpr uint32_t kTileD = L::kTile >> 4;
     auto qk = [&](int i, int stage) {
       if (lane == 0) {
+        const uint32_t aq = dq + i * kTileD, ak = dk + stage * kTileD;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t o = (k / 4) * L::kPanel + (k % 4) * 32;
-          mma_ss(tm + 128 * i,
-                 operand(base + L::kQ + i * L::kTile + o, 16, 1024),
-                 operand(base + L::kK + stage * L::kTile + o, 16, 1024), iqk,
-                 k > 0);
+          const uint32_t o = ((k / 4) * L::kPanel + (k % 4) * 32) >> 4;
+          mma_ss(tm + 128 * i, aq + o, ak + o, iqk, k > 0);
         }
         tc_commit(s_full + 8 * i);
       }
     };
-    walk(false, [&](const Ent&, int, int, int, int n, int64_t, bool two) {
+    walk(false, [&](const Ent&, int, int, int, int n, int, bool two) {
       for (int i = 0; i < (two ? 2 : 1); ++i) {
         if (!bar_wait(q_full + 8 * i, qn[i] & 1, dead)) return false;
         ++qn[i];
@@ -345,9 +369,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k)
               mma_ts(tm + 256 + 128 * i, tm + 128 * i + 8 * k,
-                     operand(base + L::kV + sv * L::kTile + k * 2048,
-                             L::kPanel, 1024),
-                     ipv, j > 0 || k > 0);
+                     dv + sv * kTileD + (k * 2048 >> 4), ipv, j > 0 || k > 0);
             if (!more) tc_commit(o_full + 8 * i);
           }
           if (more) qk(i, sk);
@@ -369,7 +391,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     const uint32_t tS = tm + lanes + 128 * slot, tO = tS + 256;
     uint32_t sn = 0, on = 0;
     walk(false, [&](const Ent& E, int tile, int h, int blk, int n,
-                    int64_t part_slot, bool two) {
+                    int part_slot, bool two) {
       if (slot == 1 && !two) return true;
       {
         // this thread's row of Q, swizzled as the tensor core expects
@@ -393,26 +415,40 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         if (!bar_wait(s_full + 8 * slot, sn & 1, dead)) return false;
         ++sn;
         tc_after();
-        uint32_t s[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tm_ld32(tS + 32 * c, s + 32 * c);
-        tm_wait_ld();
+        // The row's 128 scores pass through 64 registers: the second half
+        // first for its maximum, then the first half, whose weights are taken
+        // while it is at hand, then the second half again.  (All 128 at once
+        // spilled.)
         const int valid = E.k1 - (blk + j) * kKeys;
-        if (valid < kKeys) {
+        uint32_t s0[32], s1[32];
+        auto load = [&](int c) {
+          tm_ld32(tS + 64 * c, s0);
+          tm_ld32(tS + 64 * c + 32, s1);
+        };
+        auto mask = [&](uint32_t* s, int c) {
+          if (valid < 32 * c + 32)
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= valid) s[c] = 0xff800000u;
-        }
-        float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= valid) s[i] = 0xff800000u;
+        };
+        auto most = [&](const uint32_t* s, float t) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 8) {
-          t0 = fmaxf(t0, fmaxf(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
-          t1 = fmaxf(t1, fmaxf(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])));
-          t2 = fmaxf(t2, fmaxf(__uint_as_float(s[c + 4]), __uint_as_float(s[c + 5])));
-          t3 = fmaxf(t3, fmaxf(__uint_as_float(s[c + 6]), __uint_as_float(s[c + 7])));
-        }
-        const float top =
-            fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * a.scale_log2;
+          for (int i = 0; i < 32; i += 2)
+            t = max3(t, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+          return t;
+        };
+        load(1);
+        tm_wait_ld();
+        mask(s0, 2);
+        mask(s1, 3);
+        float t0 = most(s0, -INFINITY), t1 = most(s1, -INFINITY);
+        load(0);
+        tm_wait_ld();
+        mask(s0, 0);
+        mask(s1, 1);
+        t0 = most(s0, t0);
+        t1 = most(s1, t1);
+        const float top = fmaxf(t0, t1) * a.scale_log2;
         const bool grow = top > m + kSlack || m == -INFINITY;
         if (__any_sync(0xffffffffu, grow)) {
           const float mn = grow ? fmaxf(m, top) : m;
@@ -422,44 +458,52 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           if (j > 0) {
             // S of this block was committed behind the product before, so
             // O is at rest
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tm_ld32(tO + 32 * c, o);
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tm_ld16(tO + 16 * c, o);
               tm_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
+              for (int i = 0; i < 16; ++i)
                 o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tm_st32(tO + 32 * c, o);
+              tm_st16(tO + 16 * c, o);
             }
           }
         }
         const float neg = m == -INFINITY ? 0.f : -m;
-        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+        const float2 neg2 = make_float2(neg, neg);
+        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
+        float2 la = make_float2(0.f, 0.f), lb = la;
+        auto weights = [&](const uint32_t* s, int c) {
+          uint32_t w[16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w[32];
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float p0 = ex2t(fmaf(__uint_as_float(s[64 * c + 2 * i]),
-                                       a.scale_log2, neg));
-            const float p1 = ex2t(fmaf(__uint_as_float(s[64 * c + 2 * i + 1]),
-                                       a.scale_log2, neg));
-            const float p2 = ex2t(fmaf(__uint_as_float(s[64 * c + 2 * i + 2]),
-                                       a.scale_log2, neg));
-            const float p3 = ex2t(fmaf(__uint_as_float(s[64 * c + 2 * i + 3]),
-                                       a.scale_log2, neg));
-            l0 += p0;
-            l1 += p1;
-            l2 += p2;
-            l3 += p3;
-            // rounded to bf16 as in attend.cu; the sum takes them unrounded
-            w[i] = sv_pack(p0, p1);
-            w[i + 1] = sv_pack(p2, p3);
+          for (int i = 0; i < 16; i += 2) {
+            float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * i]),
+                                              __uint_as_float(s[2 * i + 1])),
+                                  sc2, neg2);
+            float2 y = __ffma2_rn(make_float2(__uint_as_float(s[2 * i + 2]),
+                                              __uint_as_float(s[2 * i + 3])),
+                                  sc2, neg2);
+            x = make_float2(ex2t(x.x), ex2t(x.y));
+            y = make_float2(ex2t(y.x), ex2t(y.y));
+            la = __fadd2_rn(la, x);
+            lb = __fadd2_rn(lb, y);
+            // rounded to bf16 as in attend_kernel.cuh; the sum takes them
+            // unrounded
+            w[i] = sv_pack(x.x, x.y);
+            w[i + 1] = sv_pack(y.x, y.y);
           }
-          tm_st32(tS + 32 * c, w);
-        }
-        l += (l0 + l1) + (l2 + l3);
+          tm_st16(tS + 16 * c, w);
+        };
+        weights(s0, 0);
+        weights(s1, 1);
+        load(1);
+        tm_wait_ld();
+        mask(s0, 2);
+        mask(s1, 3);
+        weights(s0, 2);
+        weights(s1, 3);
+        l += (la.x + la.y) + (lb.x + lb.y);
         tm_wait_st();
         tc_before();
         bar_arrive(p_full + 8 * slot);
@@ -468,7 +512,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       if (!bar_wait(o_full + 8 * slot, on & 1, dead)) return false;
       ++on;
       tc_after();
-      const int64_t at = part_slot * kRows + slot * 128;
+      const int64_t at = (int64_t)part_slot * kRows + slot * 128;
       a.pre.ml[at + r] = make_float2(m, l);
       float* out = a.pre.part + (at + (warp & 3) * 32) * D;
       float* stage = reinterpret_cast<float*>(

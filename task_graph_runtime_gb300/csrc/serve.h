@@ -61,8 +61,7 @@ cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t s);
 struct AttnSet {
   float* part;       // [slots][M][d]
   float2* ml;        // [slots][M]: running maximum (log2 domain) and sum
-  int32_t* ebase;    // first unit of each entity, divided by Hkv
-  int2* meta;        // per unit: first slot, number of segments
+  int2* meta;        // per unit (at meta_of): first slot, number of segments
   int64_t units, slots;   // room in meta and in part
   int M;             // rows of a tile
 };
@@ -80,7 +79,7 @@ struct AttendArgs {
   float* lse;                  // nullable [n_tokens][Hq]
   AttnSet own, pre;            // results of the sequences, of the groups
   int tc;                      // prefixes by the tensor-memory kernel
-  int wmp, wmo;                // row tiles of attend_kernel (16 x these)
+  int wmp, wmo;                // row tiles of attend_kernel: 16 x these, 8 for 0
   int box;                     // keys a TMA box takes; 0: no TMA
   CUtensorMap map_k, map_v;       // the layer's pools, if box > 0
 };
