@@ -39,7 +39,7 @@ __device__ __forceinline__ Found find(const AttendArgs& a, const AttnSet& s,
 // the partial outputs are added with their final weights, several loads in
 // flight.
 template <int D>
-__global__ void __launch_bounds__(kNT)
+__global__ void __launch_bounds__(kNT, 16)
     attend_merge(const __grid_constant__ AttendArgs a) {
   constexpr int V = D / 32;
   const PagedArgs& p = a.p;
@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kNT)
   if (w >= (int64_t)p.n_tokens * p.Hq) return;
   const int t = (int)(w / p.Hq), hq = (int)(w - (int64_t)t * p.Hq);
   const int grp = p.Hq / p.Hkv, h = hq / grp, j = hq - h * grp;
-  const int b = sv_seq_of(p.q_start, p.tokens_per_seq, p.batch, t);
+  const int b = sv_seq_of_warp(p.q_start, p.tokens_per_seq, p.batch, t);
   if (b < 0) return;                     // behind the last sequence
   const Ent own = att_seq_ent(a, b);
   const int g = a.n_groups > 0 ? att_group(a, b) : 0;
@@ -204,7 +204,23 @@ size_t attend_workspace(AttendArgs* a, char* base) {
   // the smallest row tiles that hold them; few pairs are built
   a->wmo = per <= 8 ? 0 : per <= 16 ? 1 : per <= 32 ? 2 : 4;
   a->box = attend_box(a->p);
-  a->tc = all > 64 && a->box && a->p.d >= 64 && a->scale_log2 > 0.f;
+  // The tensor-memory kernel where it is the faster one for prefixes as long
+  // as the page table allows.  Measured: it costs 8 us of its own (plan,
+  // set-up, results; the sequences' kernel starts behind it) and 1.85 us a
+  // tile of 256 rows x 128 keys on 152 SMs; the general kernel takes 2 us
+  // (head_dim 128; 64: 1.2 us) a tile of 64 x 64 on 304 CTAs.
+  if (a->n_groups && a->box && a->p.d >= 64 && a->scale_log2 > 0.f &&
+      all > 64) {
+    const double ctx = (double)a->p.page_size * a->p.max_pages;
+    const double units = (double)a->n_groups * a->p.Hkv;
+    const double gen = units * ((all + 63) / 64) * (ctx / 64) *
+                       (a->p.d == 128 ? 2.0 : 1.2) / 304;
+    const double tc =
+        8 + units * ((all + 255) / 256) * (ctx / 128) * 1.85 / 152;
+    a->tc = tc < gen;
+  } else {
+    a->tc = 0;
+  }
   a->wmp = !a->n_groups || a->tc || all <= (a->wmo ? 16 * a->wmo : 8)
                ? a->wmo
                : 4;

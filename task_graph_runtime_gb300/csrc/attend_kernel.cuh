@@ -111,7 +111,13 @@ struct Blk {
   int unit;
   int flags;           // BLK_*
 };
-enum { BLK_PREFIX = 1, BLK_FIRST = 2, BLK_LAST = 4, BLK_STOP = 8 };
+enum {
+  BLK_PREFIX = 1,
+  BLK_FIRST = 2,       // of its segment
+  BLK_LAST = 4,
+  BLK_END = 8,         // last of the CTA's stretch
+  BLK_STOP = 16        // bad arrays: no more blocks
+};
 
 __host__ __device__ constexpr int tile_rows(int wm) {
   return wm ? 16 * wm : 8;
@@ -122,9 +128,8 @@ template <int D, bool FEW = false>
 struct Cfg {
   // CTAs an SM and stages a CTA: what the consumers' registers allow; the
   // stages fill the shared memory that they share.
-  static constexpr int kCtas = FEW ? (D == 128 ? 3 : 4) : (D == 128 ? 2 : 3);
-  static constexpr int kStages =
-      FEW ? (D == 128 ? 2 : D == 64 ? 3 : 4) : (D == 128 ? 3 : 4);
+  static constexpr int kCtas = FEW && D == 128 ? 3 : D == 128 ? 2 : 4;
+  static constexpr int kStages = FEW && D == 128 ? 2 : D == 32 ? 4 : 3;
   static constexpr int kTile = kBN * D * 2;            // bytes of K (or V)
   static constexpr int kQ = 16 * D * 2;                // queries of 16 rows
   // (stages on 1024 bytes: the period of the swizzle)
@@ -142,8 +147,15 @@ struct Cfg {
 struct Cursor {
   Ent E;
   int e, nb, units, u, blk, unit0;
-  int64_t left;        // blocks of the stretch from here on
+  int64_t pos;         // its first place on the line
 };
+
+// Places of the line that a group's block takes: its time over that of a
+// sequence's block (measured with a tile of 64 rows and one of 8 or 16:
+// 3160 and 1100 cycles at head_dim 128, 2300 and 1200 at 64).
+__host__ __device__ constexpr int block_places(int d, int wmp, int wmo) {
+  return wmp == wmo ? 1 : wmo <= 1 && d == 128 ? 3 : 2;
+}
 
 // The copying warp.
 template <int D, int WMP, int WMO>
@@ -156,6 +168,7 @@ struct Copier {
   uint32_t full, empty;
   volatile int* dead;
   int G, n_ent;
+  static constexpr int W = block_places(D, WMP, WMO);
 
   __device__ __forceinline__ Ent ent(int i) const {
     return i < G ? att_group_ent(a, i) : att_seq_ent(a, i - G);
@@ -166,22 +179,20 @@ struct Copier {
     c.nb = blocks_of<kBN>(c.E);
     c.units = c.nb > 0 ? ((c.E.rows + M - 1) / M) * a.p.Hkv : 0;
   }
-  __device__ __forceinline__ void advance(Cursor& c) const {
-    --c.left;
-    if (++c.blk < c.nb) return;
-    c.blk = 0;
-    if (++c.u < c.units) return;
-    if (c.left <= 0) return;
+  __device__ __forceinline__ void next_entity(Cursor& c) const {
+    c.u = c.blk = 0;
     do {
       c.unit0 = c.e + 1 == G ? 0 : c.unit0 + c.units;
-      ++c.e;
-      if (c.e >= n_ent) {
-        c.left = 0;
-        return;
-      }
+      if (++c.e >= n_ent) return;
       enter(c);
     } while (c.units == 0);
-    c.u = 0;
+  }
+  __device__ __forceinline__ void advance(Cursor& c, int64_t end) const {
+    c.pos += c.e < G ? W : 1;
+    if (++c.blk < c.nb) return;
+    c.blk = 0;
+    if (++c.u < c.units || c.pos >= end) return;
+    next_entity(c);
   }
   __device__ __forceinline__ int first_key(const Cursor& c) const {
     return (c.E.k0 / kBN + c.blk) * kBN;
@@ -209,10 +220,17 @@ struct Copier {
     Cursor c;
     c.e = ps.e;
     c.unit0 = ps.unit0;
-    c.left = ps.x1 - ps.x0;
     enter(c);
-    c.u = (int)(ps.off / c.nb);
-    c.blk = (int)(ps.off - (int64_t)c.u * c.nb);
+    {
+      // the first block that begins in the stretch
+      const int w = c.e < G ? W : 1;
+      const int64_t i = (ps.off + w - 1) / w;
+      c.pos = ps.x0 - ps.off + i * w;
+      c.u = (int)(i / c.nb);
+      c.blk = (int)(i - (int64_t)c.u * c.nb);
+      if (c.u >= c.units) next_entity(c);
+    }
+    int64_t sent = 0;
     const int64_t dv = reinterpret_cast<const char*>(p.v) -
                        reinterpret_cast<const char*>(p.k);
     const int ch = lane % CH, r0 = lane / CH;
@@ -222,7 +240,7 @@ struct Copier {
     bool first = true;
     int st = 0;
     uint32_t ph = 1;
-    for (int64_t x = ps.x0; c.left > 0; ++x) {
+    for (bool end = false; !end; ++sent) {
       const bool prefix = c.e < G;
       const int wm = prefix ? WMP : WMO;
       Blk d;
@@ -236,17 +254,10 @@ struct Copier {
       d.unit = c.unit0 + c.u;
       const AttnSet& set = prefix ? a.pre : a.own;
       const bool stop = d.unit >= set.units;
-      const bool last = c.blk + 1 == c.nb || c.left == 1;
-      d.flags = (prefix ? BLK_PREFIX : 0) | (first ? BLK_FIRST : 0) |
+      end = c.pos + (prefix ? W : 1) >= ps.x1;
+      const bool last = c.blk + 1 == c.nb || end;
+      d.flags = (end ? BLK_END : 0) | (prefix ? BLK_PREFIX : 0) | (first ? BLK_FIRST : 0) |
                 (last ? BLK_LAST : 0) | (stop ? BLK_STOP : 0);
-      if (lane == 0 && c.blk == 0 && !stop) {
-        const int end = plan_owner(x + c.nb - 1, ps.total, ps.n);
-        const int64_t at = meta_of(p, d.tok0, prefix ? c.e : c.e - G, d.tile,
-                                   tile_rows(wm), d.h);
-        if (at < set.units)
-          set.meta[at] =
-              make_int2(d.unit + (int)blockIdx.x, end - (int)blockIdx.x + 1);
-      }
       // rows of the pool (32-bit numbers: 2^32 rows of 64 bytes are more
       // than the memory)
       uint32_t row[2];
@@ -260,28 +271,19 @@ struct Copier {
                     : 0xffffffffu;
       }
       // the next block's pages, on the way while this one waits for its stage
-      advance(c);
-      if (c.left > 0) pages(c, pg);
+      const bool starts = c.blk == 0;
+      const int ent_ = c.e, nb = c.nb;
+      const int64_t pos = c.pos;
+      if (!end) {
+        advance(c, ps.x1);
+        pages(c, pg);
+      }
       if (!bar_wait(empty + 8 * st, ph, dead)) break;
       const uint32_t ks = t_addr(smem + st * C::kStage);
-      if (first && wm <= 1 && !stop) {
-#pragma unroll
-        for (int i = 0; i < 16 / RW; ++i) {
-          const int r = r0 + i * RW, rw = d.tile * tile_rows(wm) + r;
-          if (wm == 0 && r >= 8) break;
-          const bool ok = rw < d.rows;
-          const int tok = ok ? rw / grp : 0;
-          cp16(ks + 2 * C::kTile + swz<D, 16>(r, ch),
-               a.q + (d.tok0 + tok) * a.q_stride +
-                   (int64_t)(d.h * grp + (ok ? rw - tok * grp : 0)) * D +
-                   ch * 8,
-               ok ? 16 : 0);
-        }
-      }
-      uint32_t bytes = 0;
       if (a.box) {
         const bool ok = row[0] != 0xffffffffu;
-        bytes = __popc(__ballot_sync(0xffffffffu, ok)) * a.box * D * 4;
+        const uint32_t bytes =
+            __popc(__ballot_sync(0xffffffffu, ok)) * a.box * D * 4;
         // (the bytes are announced first)
         if (lane == 0) {
           blk[st] = d;
@@ -298,7 +300,6 @@ struct Copier {
                    (int)row[0], full + 8 * st);
           }
         }
-        cp_arrive(full + 8 * st);
       } else {
         const char* kp = reinterpret_cast<const char*>(p.k) + ch * 16;
 #pragma unroll 4
@@ -313,11 +314,34 @@ struct Copier {
           cp16(dst, src, ok ? 16 : 0);
           cp16(dst + C::kTile, src + dv, ok ? 16 : 0);
         }
-        cp_arrive(full + 8 * st);
         if (lane == 0) {
           blk[st] = d;
           bar_arrive(full + 8 * st);
         }
+      }
+      if (first && wm <= 1 && !stop) {
+#pragma unroll
+        for (int i = 0; i < 16 / RW; ++i) {
+          const int r = r0 + i * RW, rw = d.tile * tile_rows(wm) + r;
+          if (wm == 0 && r >= 8) break;
+          const bool ok = rw < d.rows;
+          const int tok = ok ? (int)sv_div(rw, p.grp_div) : 0;
+          cp16(ks + 2 * C::kTile + swz<D, 16>(r, ch),
+               a.q + (d.tok0 + tok) * a.q_stride +
+                   (int64_t)(d.h * grp + (ok ? rw - tok * grp : 0)) * D +
+                   ch * 8,
+               ok ? 16 : 0);
+        }
+      }
+      cp_arrive(full + 8 * st);
+      if (lane == 0 && starts && !stop) {
+        const int to = plan_owner(pos + (int64_t)(nb - 1) * (prefix ? W : 1),
+                                  ps.total, ps.n);
+        const int64_t at = meta_of(p, d.tok0, prefix ? ent_ : ent_ - G, d.tile,
+                                   tile_rows(wm), d.h);
+        if (at < set.units)
+          set.meta[at] =
+              make_int2(d.unit + (int)blockIdx.x, to - (int)blockIdx.x + 1);
       }
       if (stop) {   // q_start or group_start not ascending
         sv_latch(p.status, MPK_ERR_INVALID_ARG);
@@ -332,7 +356,6 @@ struct Copier {
     cp_wait_all();
     // no box may land after the CTA has left
     int late = 0;
-    const int64_t sent = ps.x1 - ps.x0 - c.left;
     for (int64_t i = sent < C::kStages ? 0 : sent - C::kStages;
          a.box && i < sent; ++i)
       bar_wait(full + 8 * (int)(i % C::kStages),
@@ -876,14 +899,33 @@ struct Attend {
   template <int WMP, int WMO>
   __device__ __forceinline__ void run(const Blk* blk, uint32_t full,
                                       uint32_t empty, volatile int* dead,
-                                      int64_t n) {
+                                      bool starts_prefix) {
     int st = 0;
     uint32_t ph = 0;
     Seg sg;
-    for (int64_t x = 0; x < n; ++x) {
-      if (!bar_wait(full + 8 * st, ph, dead)) return;
-      const Blk b = blk[st];
-      if (b.flags & BLK_STOP) return;
+    // A turn without a block while the first one is on its way: it brings the
+    // loop's code into the instruction caches (a first block took 5000
+    // cycles, the next ones 1100).  It reads whatever the stage holds and
+    // writes nothing; begin() sets the state anew.
+    bool warm = true;
+    sg.k0 = 0;
+    sg.k1 = sg.lim[0] = sg.lim[1] = sg.lim_min = 0x7fffffff;
+    sg.prefix = true;
+    m[0] = m[1] = l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) qf[i][0] = qf[i][1] = qf[i][2] = qf[i][3] = 0u;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    while (true) {
+      Blk b;
+      if (warm) {
+        b.key = b.unit = b.rows = b.tile = 0;
+        b.flags = starts_prefix ? BLK_PREFIX : 0;
+      } else {
+        if (!bar_wait(full + 8 * st, ph, dead)) return;
+        b = blk[st];
+        if (b.flags & BLK_STOP) return;
+      }
       const bool prefix = b.flags & BLK_PREFIX;
       const AttnSet& set = prefix ? a.pre : a.own;
       const int64_t slot = (int64_t)b.unit + blockIdx.x;
@@ -892,8 +934,13 @@ struct Attend {
       } else {
         step<WMO>(sg, b, set, slot, st);
       }
+      if (warm) {
+        warm = false;
+        continue;
+      }
       __syncwarp();
       if ((threadIdx.x & 31) == 0) bar_arrive(empty + 8 * st);
+      if (b.flags & BLK_END) return;
       if (++st == C::kStages) {
         st = 0;
         ph ^= 1u;
@@ -913,6 +960,10 @@ __global__ void __launch_bounds__(kNT, WMP > 1 ? 2 : Cfg<D, WMP == 0>::kCtas)
   __shared__ __align__(8) uint64_t bars[2 * kStages];
   __shared__ int s_dead;
   const uint32_t full = t_addr(bars), empty = full + 8 * kStages;
+  if (threadIdx.x == kComp && a.box) {
+    prefetch_map(&a.map_k);
+    prefetch_map(&a.map_v);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       bar_init(full + 8 * i, 33);      // the copying lanes and one of them
@@ -930,7 +981,8 @@ __global__ void __launch_bounds__(kNT, WMP > 1 ? 2 : Cfg<D, WMP == 0>::kCtas)
                          empty, &s_dead, a.tc ? 0 : a.n_groups, 0};
   cp.n_ent = cp.G + a.p.batch;
   // (its barriers also publish the initialisation above)
-  const PlanStart ps = plan_start<kNT, tile_rows(WMP), tile_rows(WMO), kBN>(
+  const PlanStart ps = plan_start<kNT, tile_rows(WMP), tile_rows(WMO), kBN,
+                                  block_places(D, WMP, WMO)>(
       cp.G, cp.n_ent, a.p.Hkv, [&](int i) { return cp.ent(i); }, blockIdx.x,
       gridDim.x);
   if (ps.x0 < ps.x1) {
@@ -938,7 +990,7 @@ __global__ void __launch_bounds__(kNT, WMP > 1 ? 2 : Cfg<D, WMP == 0>::kCtas)
       cp.run(ps);
     } else {
       Attend<D, WMP == 0> t{a, smem, s_ml};
-      t.template run<WMP, WMO>(s_blk, full, empty, &s_dead, ps.x1 - ps.x0);
+      t.template run<WMP, WMO>(s_blk, full, empty, &s_dead, ps.e < cp.G);
     }
     __syncthreads();
     if (threadIdx.x == 0 && s_dead) sv_latch(a.p.status, MPK_ERR_TIMEOUT);
@@ -950,8 +1002,8 @@ template <int D, int WMP, int WMO>
 cudaError_t run_tiles(const AttendArgs& a, cudaStream_t s) {
   using C = Cfg<D, WMP == 0>;
   auto k = attend_kernel<D, WMP, WMO>;
-  cudaError_t e = cudaFuncSetAttribute(
-      k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static SmemLimit limit;
+  cudaError_t e = limit.set((const void*)k, C::kSmem);
   if (e != cudaSuccess) return e;
   const int ctas = WMP > 1 ? 2 : C::kCtas;
   return sv_launch(k, dim3(attend_ctas() / 4 * ctas), kNT, C::kSmem, s, a);

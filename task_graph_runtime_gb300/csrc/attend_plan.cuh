@@ -7,7 +7,8 @@
 // is one (row tile, KV head), numbered among the groups' or the sequences'.
 // All blocks of all units form one line, of which every CTA takes an equal
 // stretch: the load is even whatever the lengths are, and a long key axis is
-// split when there are few rows.  A stretch of one unit's blocks is a
+// split when there are few rows.  A group's block takes W places of the line
+// (what its larger row tile costs), and belongs to the CTA with its first.  A stretch of one unit's blocks is a
 // segment; its partial result goes to slot (unit + CTA), which is unique
 // because along the line either number grows from one segment to the next.
 // The unit's slots are consecutive, so the merge needs only the first and
@@ -80,6 +81,9 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map,
       "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -165,8 +169,8 @@ __device__ __forceinline__ int64_t meta_of(const PagedArgs& p, int tok0, int e,
 // Where a CTA starts on the line.
 struct PlanStart {
   int64_t x0, x1;      // this CTA's stretch
-  int64_t total;       // blocks of all units
-  int64_t off;         // x0 within entity e
+  int64_t total;       // places of all units
+  int64_t off;         // x0 within entity e, in places
   int unit0;           // units before entity e, of its kind
   int e;
   int n;               // CTAs that take part
@@ -175,7 +179,7 @@ struct PlanStart {
 // Finds the CTA's stretch with one scan over the entities (NT threads).
 // Both passes of a batch of more than NT entities read the arrays again.
 // `ent(e)` gives entity e; the first G are groups.
-template <int NT, int MP, int MO, int BN, typename F>
+template <int NT, int MP, int MO, int BN, int W, typename F>
 __device__ __forceinline__ PlanStart plan_start(int G, int n_ent, int Hkv,
                                                 F ent, int cta, int n_cta) {
   __shared__ int64_t sh_cost[NT / 32], sh_unit[NT / 32];
@@ -189,39 +193,15 @@ __device__ __forceinline__ PlanStart plan_start(int G, int n_ent, int Hkv,
       const int64_t nb = blocks_of<BN>(e);
       const int64_t nt =
           i < G ? (e.rows + MP - 1) / MP : (e.rows + MO - 1) / MO;
-      cost = nb * nt * Hkv;
+      cost = nb * nt * Hkv * (i < G ? W : 1);
       // groups in the low half, sequences in the high half
       unit = nb > 0 ? nt * Hkv : 0;
       if (i >= G) unit <<= 32;
     }
   };
-  int64_t cost, unit, total = 0;
-  blocks(tid, cost, unit);
-  {
-    int64_t mine = cost, c2, u2;
-    for (int i = tid + NT; i < n_ent; i += NT) {
-      blocks(i, c2, u2);
-      mine += c2;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) sh_cost[warp] = mine;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) total += sh_cost[w];
-  }
-  PlanStart st;
-  st.total = total;
-  // every CTA that takes part has a block, so a unit's segments belong to
-  // consecutive CTAs
-  st.n = total < n_cta ? (int)total : n_cta;
-  st.x0 = cta < st.n ? total * cta / st.n : total;
-  st.x1 = cta < st.n ? total * (cta + 1) / st.n : total;
-  if (tid == 0) sh_e = n_ent;
-  int64_t run_c = 0, run_u = 0;
-  for (int i0 = 0; i0 < n_ent; i0 += NT) {
-    if (i0 > 0) blocks(i0 + tid, cost, unit);
+  // prefix sums over NT entities: this thread's (exclusive) and the sum
+  auto scan = [&](int64_t& cost, int64_t& unit, int64_t& sum_c,
+                  int64_t& sum_u) {
     int64_t ic = cost, iu = unit;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -232,30 +212,73 @@ __device__ __forceinline__ PlanStart plan_start(int G, int n_ent, int Hkv,
         iu += vu;
       }
     }
-    __syncthreads();
     if (lane == 31) {
       sh_cost[warp] = ic;
       sh_unit[warp] = iu;
     }
     __syncthreads();
-    int64_t bc = run_c, bu = run_u;
+    int64_t bc = 0, bu = 0;
+    sum_c = sum_u = 0;
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) {
+      const int64_t wc = sh_cost[w], wu = sh_unit[w];
       if (w < warp) {
-        bc += sh_cost[w];
-        bu += sh_unit[w];
+        bc += wc;
+        bu += wu;
       }
-      run_c += sh_cost[w];
-      run_u += sh_unit[w];
+      sum_c += wc;
+      sum_u += wu;
     }
-    bc += ic - cost;
-    bu += iu - unit;
-    if (cost > 0 && st.x0 >= bc && st.x0 < bc + cost) {
-      sh_e = i0 + tid;
+    cost = bc + ic - cost;
+    unit = bu + iu - unit;
+  };
+  if (tid == 0) sh_e = n_ent;
+  int64_t cost, unit, bc, bu, total, units;
+  blocks(tid, cost, unit);
+  bc = cost;
+  bu = unit;
+  scan(bc, bu, total, units);
+  int64_t more = 0;
+  for (int i0 = NT; i0 < n_ent; i0 += NT) {
+    int64_t c2, u2, s2, v2;
+    blocks(i0 + tid, c2, u2);
+    __syncthreads();
+    scan(c2, u2, s2, v2);
+    more += s2;
+  }
+  const int64_t first = total;   // of the first NT entities
+  total += more;
+  PlanStart st;
+  st.total = total;
+  // every CTA that takes part has a block, so a unit's segments belong to
+  // consecutive CTAs
+  st.n = total / W < n_cta ? max((int)(total / W), 1) : n_cta;
+  if (total <= 0xffffffffll / (n_cta + 1)) {
+    const uint32_t t = (uint32_t)total, n = (uint32_t)st.n;
+    st.x0 = cta < st.n ? t * (uint32_t)cta / n : t;
+    st.x1 = cta < st.n ? t * (uint32_t)(cta + 1) / n : t;
+  } else {
+    st.x0 = cta < st.n ? total * cta / st.n : total;
+    st.x1 = cta < st.n ? total * (cta + 1) / st.n : total;
+  }
+  auto here = [&](int i, int64_t c, int64_t bc, int64_t bu) {
+    if (c > 0 && st.x0 >= bc && st.x0 < bc + c) {
+      sh_e = i;
       sh_off = st.x0 - bc;
       sh_base = bu;
     }
-    if (run_c > st.x0) break;
+  };
+  here(tid, cost, bc, bu);
+  int64_t run_c = first, run_u = units;
+  for (int i0 = NT; i0 < n_ent && run_c <= st.x0; i0 += NT) {
+    int64_t c2, u2, s2, v2;
+    blocks(i0 + tid, c2, u2);
+    int64_t e2 = c2;
+    __syncthreads();
+    scan(e2, u2, s2, v2);
+    here(i0 + tid, c2, run_c + e2, run_u + u2);
+    run_c += s2;
+    run_u += v2;
   }
   __syncthreads();
   st.e = sh_e;
@@ -267,6 +290,8 @@ __device__ __forceinline__ PlanStart plan_start(int G, int n_ent, int Hkv,
 // CTA that owns position x of the line.
 __device__ __forceinline__ int plan_owner(int64_t x, int64_t total,
                                           int n_cta) {
+  if (total <= 0xffffffffll / (n_cta + 1))
+    return (int)(((uint32_t)(x + 1) * (uint32_t)n_cta - 1) / (uint32_t)total);
   return (int)(((x + 1) * n_cta - 1) / total);
 }
 

@@ -182,6 +182,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 8) {
+    prefetch_map(&a.map_k);
+    prefetch_map(&a.map_v);
     asm volatile(
         "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::
             "r"(t_addr(&s_tmem))
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   const PagedArgs& p = a.p;
   const int box = a.box;
   const int Hkv = p.Hkv, grp = p.Hq / p.Hkv;
-  const PlanStart st = plan_start<kThreadsT, kRows, kRows, kKeys>(
+  const PlanStart st = plan_start<kThreadsT, kRows, kRows, kKeys, 1>(
       a.n_groups, a.n_groups, Hkv, [&](int g) { return att_group_ent(a, g); }, blockIdx.x,
       gridDim.x);
   volatile int* dead = &s_dead;
@@ -393,20 +395,22 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     walk(false, [&](const Ent& E, int tile, int h, int blk, int n,
                     int part_slot, bool two) {
       if (slot == 1 && !two) return true;
-      {
-        // this thread's row of Q, swizzled as the tensor core expects
-        const int row = tile * kRows + slot * 128 + r;
-        uint8_t* q = smem + L::kQ + slot * L::kTile;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + (E.tok0 + (row < E.rows ? row / grp : 0)) * a.q_stride +
-            (int64_t)(h * grp + (row < E.rows ? row % grp : 0)) * D);
+      // the slot's rows of Q, swizzled as the tensor core expects: D / 8
+      // neighbouring threads a row
+      uint8_t* q = smem + L::kQ + slot * L::kTile;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 u =
-              row < E.rows ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(q + (c / 8) * L::kPanel + r * 128 +
-                                    (((c & 7) ^ (r & 7)) << 4)) = u;
+      for (int k = 0; k < D / 8; ++k) {
+        const int i = k * 128 + r, rr = i / (D / 8), c = i % (D / 8);
+        const int row = tile * kRows + slot * 128 + rr;
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (row < E.rows) {
+          const int tok = (int)sv_div(row, p.grp_div);
+          u = __ldg(reinterpret_cast<const uint4*>(
+              a.q + (E.tok0 + tok) * a.q_stride +
+              (int64_t)(h * grp + row - tok * grp) * D + c * 8));
         }
+        *reinterpret_cast<uint4*>(q + (c / 8) * L::kPanel + rr * 128 +
+                                  (((c & 7) ^ (rr & 7)) << 4)) = u;
       }
       fence_async();
       bar_arrive(q_full + 8 * slot);
@@ -514,6 +518,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       tc_after();
       const int64_t at = (int64_t)part_slot * kRows + slot * 128;
       a.pre.ml[at + r] = make_float2(m, l);
+      // through shared memory (over Q, which the products have finished
+      // with), so that rows leave in whole lines
       float* out = a.pre.part + (at + (warp & 3) * 32) * D;
       float* stage = reinterpret_cast<float*>(
           smem + (L::kOver ? L::kExtra + warp * L::kStage
@@ -552,9 +558,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 
 template <int D>
 cudaError_t tc_d(const AttendArgs& a, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(
-      attend_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      TcSmem<D>::kSmem);
+  static SmemLimit limit;
+  cudaError_t e = limit.set((const void*)attend_tc<D>, TcSmem<D>::kSmem);
   if (e != cudaSuccess) return e;
   return sv_launch(attend_tc<D>, dim3(attend_tc_ctas()), kThreadsT,
                    TcSmem<D>::kSmem, s, a);

@@ -30,7 +30,7 @@ struct PagedArgs {
   int tokens_per_seq;          // rows of a sequence when q_start is null
   int batch, n_tokens;
   int num_pages, page_size, max_pages;
-  FastDiv page_div;
+  FastDiv page_div, grp_div;   // by page_size; by query heads per KV head
   int Hq, Hkv, d;
   uint32_t* status;            // nullable: first error found
 };

@@ -70,6 +70,7 @@ mpk_status fill_paged(const mpk_attn_shape* s, const mpk_token_batch* t,
   p->page_size = s->page_size;
   p->max_pages = s->max_pages_per_seq;
   p->page_div = fast_div((uint32_t)s->page_size);
+  p->grp_div = fast_div((uint32_t)(s->n_q_heads / s->n_kv_heads));
   p->Hq = s->n_q_heads;
   p->Hkv = s->n_kv_heads;
   p->d = s->head_dim;
@@ -171,6 +172,7 @@ size_t mpk_prefix_attention_workspace(const mpk_attn_shape* shape,
   a.p.batch = tok->batch;
   a.p.n_tokens = tok->n_tokens;
   a.p.page_size = shape->page_size;
+  a.p.max_pages = shape->max_pages_per_seq;
   a.p.Hq = shape->n_q_heads;
   a.p.Hkv = shape->n_kv_heads;
   a.p.d = shape->head_dim;

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "mpk.h"
 #include "serve.h"
 
@@ -78,6 +80,22 @@ __device__ __forceinline__ int sv_seq_of_warp(const int32_t* q_start, int per,
   }
   return n < batch ? n : -1;
 }
+
+// Raises a kernel's limit of dynamic shared memory, once a device.
+struct SmemLimit {
+  std::atomic<bool> done[64] = {};
+  cudaError_t set(const void* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev < 64;
+    if (known && done[dev].load(std::memory_order_relaxed)) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             bytes);
+    if (e == cudaSuccess && known) done[dev].store(true);
+    return e;
+  }
+};
 
 // Launch with the attribute that lets the kernel's preamble overlap the end
 // of the kernel before it in the stream (which must call sv_grid_wait before

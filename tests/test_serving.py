@@ -175,7 +175,7 @@ class Case:
     """A ragged batch over a paged cache on the GPU, with float64 copies."""
 
     def __init__(self, seed, n, ctx, hq=4, hkv=2, d=64, page=16, layers=2,
-                 layer=1, groups=None, pad=0, spare=3, stale=None):
+                 layer=1, groups=None, pad=0, spare=3, stale=None, wide=0):
         g = np.random.Generator(np.random.PCG64(seed))
         self.n, self.ctx, self.page, self.layer = n, ctx, page, layer
         self.hq, self.hkv, self.d = hq, hkv, d
@@ -188,7 +188,7 @@ class Case:
         self.first = [cut[i] for i in range(len(pre))
                       for _ in range(cut[i], cut[i + 1])]
         need = [-(-(c + m) // page) for c, m in zip(ctx, n)]
-        cols = max(max(need), 1) + 1
+        cols = max(max(need), 1) + 1 + wide
         pages, rows = 0, []
         for b in range(B):
             share = self.prefix[b] // page if b != self.first[b] else 0
@@ -285,7 +285,10 @@ ATTEND = {
                  groups=([0, 50, 150], [0, 147])),
 }
 
-# groups with more rows than a sequence: the prefix has launches of its own
+# Groups with more rows than a sequence.  A page table that could hold long
+# prefixes (WIDE columns more) gives groups of more than 64 rows a kernel of
+# their own.
+WIDE = 100_000
 PREFIX = {
     "one_block": dict(n=[1] * 20, ctx=[100] * 20, d=128, hq=8,
                       groups=([0, 20], [100])),
@@ -312,9 +315,10 @@ PREFIX = {
 
 
 @gpu
+@pytest.mark.parametrize("wide", [0, WIDE])
 @pytest.mark.parametrize("name", sorted(PREFIX))
-def test_attend_prefix_launches(name):
-    c = Case(41, **PREFIX[name])
+def test_attend_prefix_launches(name, wide):
+    c = Case(41, wide=wide, **PREFIX[name])
     out, lse = c.attend()
     assert c.status.item() == 0
     c.check(out, lse)
@@ -325,8 +329,9 @@ def test_attend_prefix_launches(name):
 @gpu
 @pytest.mark.parametrize("name", ["tiles", "d64", "page100"])
 @pytest.mark.parametrize("stale", [math.nan, -math.inf])
-def test_attend_prefix_launches_stale_slots(name, stale):
-    c = Case(42, stale=stale, **PREFIX[name])
+@pytest.mark.parametrize("wide", [0, WIDE])
+def test_attend_prefix_launches_stale_slots(name, stale, wide):
+    c = Case(42, stale=stale, wide=wide, **PREFIX[name])
     out, lse = c.attend()
     c.check(out, lse)
     assert torch.isfinite(out[:c.T].float()).all()
@@ -334,17 +339,20 @@ def test_attend_prefix_launches_stale_slots(name, stale):
 
 @gpu
 @pytest.mark.parametrize("scale", [2.0, -0.3])
-def test_attend_prefix_launches_scale(scale):
+@pytest.mark.parametrize("wide", [0, WIDE])
+@pytest.mark.parametrize("name", ["page64_long", "two_slots"])
+def test_attend_prefix_launches_scale(scale, wide, name):
     # large scores: the running maximum grows often; a negative scale
-    c = Case(43, **PREFIX["page64_long"])
+    c = Case(43, wide=wide, **PREFIX[name])
     out, lse = c.attend(scale=scale)
     c.check(out, lse, scale)
 
 
 @gpu
-def test_attend_prefix_launches_growing_maximum():
+@pytest.mark.parametrize("wide", [0, WIDE])
+def test_attend_prefix_launches_growing_maximum(wide):
     # keys that grow along the prefix: every block raises the maximum
-    c = Case(44, **PREFIX["tiles"])
+    c = Case(44, wide=wide, **PREFIX["tiles"])
     t = torch.arange(300, device="cuda").float().div(40)
     for b in [0]:
         row = torch.from_numpy(c.table[b].astype(np.int64)).cuda()
@@ -356,8 +364,9 @@ def test_attend_prefix_launches_growing_maximum():
 
 
 @gpu
-def test_attend_prefix_launches_missing_page():
-    c = Case(45, n=[1] * 40, ctx=[200] * 40, d=128, hq=8,
+@pytest.mark.parametrize("wide", [0, WIDE])
+def test_attend_prefix_launches_missing_page(wide):
+    c = Case(45, n=[1] * 40, ctx=[200] * 40, d=128, hq=8, wide=wide,
              groups=([0, 20, 40], [128, 128]))
     want, _ = c.attend()
     c.kv.page_table[0, 3] = -1
