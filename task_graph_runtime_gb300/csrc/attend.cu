@@ -14,32 +14,36 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Where the segments of a row's unit are: slots [first, first + n).
+// The segments of a row's unit: the row in the first slot (an index into ml),
+// and how many slots.
 struct Found {
-  int64_t at;          // row 0's index into ml (in rows) of the first slot
+  int64_t at;
   int n;
 };
 __device__ __forceinline__ Found find(const AttendArgs& a, const AttnSet& s,
                                       int tok0, int e, int row, int h) {
   Found f{0, 0};
   if (row < 0) return f;
-  const int tile = row / s.M;
-  const int64_t at = meta_of(a.p, tok0, e, tile, s.M, h);
+  const int tile = row >> s.shift;
+  const int64_t at = meta_of(a.p, tok0, e, tile, s.shift, h);
   if (at >= s.units) return f;
   const int2 me = s.meta[at];
   // (only arrays that are not ascending leave anything else here)
   if (me.x < 0 || me.y < 0 || me.y > s.slots - me.x) return f;
-  f.at = (int64_t)me.x * s.M + (row - tile * s.M);
+  f.at = ((int64_t)me.x << s.shift) + (row & (s.M - 1));
   f.n = me.y;
   return f;
 }
 
 // One warp joins the segments of one (token, query head): the prefix's and
 // the sequence's own.  Lane i fetches the maximum and sum of segment i, then
-// the partial outputs are added with their final weights, several loads in
-// flight.
+// the partial outputs are added with their final weights, four loads in
+// flight.  A small grid goes through one turn of the same code on whatever
+// the workspace holds while it waits for the kernels before it, so that the
+// instructions and the pages' translations are at hand.  (Four heads a warp
+// took 6 us longer with 16 sequences, and as long with 256.)
 template <int D>
-__global__ void __launch_bounds__(kNT, 16)
+__global__ void __launch_bounds__(kNT)
     attend_merge(const __grid_constant__ AttendArgs a) {
   constexpr int V = D / 32;
   const PagedArgs& p = a.p;
@@ -47,69 +51,76 @@ __global__ void __launch_bounds__(kNT, 16)
   const int64_t w = (int64_t)blockIdx.x * (kNT / 32) + (threadIdx.x >> 5);
   if (w >= (int64_t)p.n_tokens * p.Hq) return;
   const int t = (int)(w / p.Hq), hq = (int)(w - (int64_t)t * p.Hq);
-  const int grp = p.Hq / p.Hkv, h = hq / grp, j = hq - h * grp;
+  const int h = (int)sv_div(hq, p.grp_div), grp = p.Hq / p.Hkv;
+  const int j = hq - h * grp;
   const int b = sv_seq_of_warp(p.q_start, p.tokens_per_seq, p.batch, t);
   if (b < 0) return;                     // behind the last sequence
   const Ent own = att_seq_ent(a, b);
   const int g = a.n_groups > 0 ? att_group(a, b) : 0;
   Ent pre{0, 0, 0, 0, 0};
   if (a.n_groups > 0) pre = att_group_ent(a, g);
-  sv_grid_wait();
-  Found fp{0, 0}, fo{0, 0};
-  if (pre.k1 > 0)
-    fp = find(a, a.pre, pre.tok0, g, (t - pre.tok0) * grp + j, h);
-  if (own.k1 > own.k0)
-    fo = find(a, a.own, own.tok0, b, (t - own.tok0) * grp + j, h);
-  const int n = fp.n + fo.n;
-  float m = -INFINITY, l = 0.f, acc[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const int i = i0 + lane;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    const float* src = nullptr;
-    if (i < n) {
-      const bool q = i < fp.n;
-      const AttnSet& s = q ? a.pre : a.own;
-      const int64_t at =
-          q ? fp.at + (int64_t)i * s.M : fo.at + (int64_t)(i - fp.n) * s.M;
-      ml = s.ml[at];
-      src = s.part + at * D;
+  float m, l, acc[V];
+  for (int pass = gridDim.x <= 152 * 2 ? 0 : 1; pass < 2; ++pass) {
+    Found fp{0, 0}, fo{0, 1};            // (every set has a slot)
+    if (pass == 1) {
+      sv_grid_wait();
+      fo.n = 0;
+      if (pre.k1 > 0)
+        fp = find(a, a.pre, pre.tok0, g, (t - pre.tok0) * grp + j, h);
+      if (own.k1 > own.k0)
+        fo = find(a, a.own, own.tok0, b, (t - own.tok0) * grp + j, h);
     }
-    float top = ml.x;
+    const int n = fp.n + fo.n;
+    m = -INFINITY;
+    l = 0.f;
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1)
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-    const float mn = fmaxf(m, top);
-    const float f = mn == -INFINITY ? 0.f : ex2(m - mn);
-    const float wt = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn);
-    float sum = ml.x == -INFINITY ? 0.f : ml.y * wt;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1)
-      sum += __shfl_xor_sync(0xffffffffu, sum, s);
-    m = mn;
-    l = l * f + sum;
-#pragma unroll
-    for (int q = 0; q < V; ++q) acc[q] *= f;
-    const int k = min(32, n - i0);
-#pragma unroll 4
-    for (int q = 0; q < k; ++q) {
-      const float* s = reinterpret_cast<const float*>(__shfl_sync(
-          0xffffffffu, reinterpret_cast<unsigned long long>(src), q));
-      const float x = __shfl_sync(0xffffffffu, wt, q);
-      float v[V];
-      if constexpr (V == 4) {
-        const float4 u = *reinterpret_cast<const float4*>(s + lane * 4);
-        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-      } else if constexpr (V == 2) {
-        const float2 u = *reinterpret_cast<const float2*>(s + lane * 2);
-        v[0] = u.x; v[1] = u.y;
-      } else {
-        v[0] = s[lane];
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      const float* src = nullptr;
+      if (i < n) {
+        const bool q = i < fp.n;
+        const int64_t at = q ? fp.at + ((int64_t)i << a.pre.shift)
+                             : fo.at + ((int64_t)(i - fp.n) << a.own.shift);
+        ml = q ? a.pre.ml[at] : a.own.ml[at];
+        src = (q ? a.pre.part : a.own.part) + at * D;
       }
-      // a segment in which the row saw nothing has weight 0 and zeros
+      float top = ml.x;
 #pragma unroll
-      for (int c = 0; c < V; ++c) acc[c] = fmaf(v[c], x, acc[c]);
+      for (int s = 16; s > 0; s >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+      const float mn = fmaxf(m, top);
+      const float f = mn == -INFINITY ? 0.f : ex2(m - mn);
+      const float wt = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn);
+      float sum = ml.x == -INFINITY ? 0.f : ml.y * wt;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, s);
+      m = mn;
+      l = l * f + sum;
+#pragma unroll
+      for (int q = 0; q < V; ++q) acc[q] *= f;
+      const int k = min(32, n - i0);
+#pragma unroll 4
+      for (int q = 0; q < k; ++q) {
+        const float* s = reinterpret_cast<const float*>(__shfl_sync(
+            0xffffffffu, reinterpret_cast<unsigned long long>(src), q));
+        const float x = __shfl_sync(0xffffffffu, wt, q);
+        float v[V];
+        if constexpr (V == 4) {
+          const float4 u = *reinterpret_cast<const float4*>(s + lane * 4);
+          v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+        } else if constexpr (V == 2) {
+          const float2 u = *reinterpret_cast<const float2*>(s + lane * 2);
+          v[0] = u.x; v[1] = u.y;
+        } else {
+          v[0] = s[lane];
+        }
+        // a segment in which the row saw nothing has weight 0 and zeros
+#pragma unroll
+        for (int c = 0; c < V; ++c) acc[c] = fmaf(v[c], x, acc[c]);
+      }
     }
   }
   // no key seen: zeros, and -inf for the log sum
@@ -126,9 +137,7 @@ __global__ void __launch_bounds__(kNT, 16)
   }
   if (a.lse && lane == 0)
     a.lse[(int64_t)t * p.Hq + hq] =
-        l == 0.f ? -INFINITY
-                 : (float)(((double)m + (double)log2f(l)) *
-                           0.69314718055994530942);
+        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
@@ -228,6 +237,7 @@ size_t attend_workspace(AttendArgs* a, char* base) {
   a->pre.M = a->tc ? attend_tc_rows() : a->wmp ? 16 * a->wmp : 8;
   // a set holds the results of n entities whose rows are disjoint
   auto place = [&](AttnSet* s, int64_t n, int ctas) {
+    s->shift = 31 - __builtin_clz((unsigned)s->M);
     s->units = (rows / s->M + n) * a->p.Hkv;
     s->slots = s->units + ctas;
     s->meta = reinterpret_cast<int2*>(take(s->units * 8));

@@ -338,7 +338,7 @@ struct Copier {
         const int to = plan_owner(pos + (int64_t)(nb - 1) * (prefix ? W : 1),
                                   ps.total, ps.n);
         const int64_t at = meta_of(p, d.tok0, prefix ? ent_ : ent_ - G, d.tile,
-                                   tile_rows(wm), d.h);
+                                   set.shift, d.h);
         if (at < set.units)
           set.meta[at] =
               make_int2(d.unit + (int)blockIdx.x, to - (int)blockIdx.x + 1);

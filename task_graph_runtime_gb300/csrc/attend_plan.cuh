@@ -161,9 +161,10 @@ __device__ __forceinline__ int blocks_of(const Ent& e) {
 // looking anything up.  Tiles of entity e (of its kind) begin at row
 // tok0 * heads of all rows; the entities' tiles do not meet because each
 // entity adds one to the quotient.  Below rows / M + entities.
+// (Rows of a KV head and entities times KV heads are below 2^30.)
 __device__ __forceinline__ int64_t meta_of(const PagedArgs& p, int tok0, int e,
-                                           int tile, int M, int h) {
-  return ((int64_t)tok0 * (p.Hq / p.Hkv) / M + e + tile) * p.Hkv + h;
+                                           int tile, int shift, int h) {
+  return (int64_t)((tok0 * (p.Hq / p.Hkv) >> shift) + e + tile) * p.Hkv + h;
 }
 
 // Where a CTA starts on the line.

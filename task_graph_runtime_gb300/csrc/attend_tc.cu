@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       }
       if (writes_meta && blk == 0) {
         const int last = plan_owner(st.x1 - left + nb - 1, st.total, st.n);
-        const int64_t at = meta_of(p, E.tok0, e, tile, kRows, u - tile * Hkv);
+        const int64_t at = meta_of(p, E.tok0, e, tile, a.pre.shift, u - tile * Hkv);
         if (at < a.pre.units)
           a.pre.meta[at] =
               make_int2(unit + (int)blockIdx.x, last - (int)blockIdx.x + 1);

@@ -63,7 +63,7 @@ struct AttnSet {
   float2* ml;        // [slots][M]: running maximum (log2 domain) and sum
   int2* meta;        // per unit (at meta_of): first slot, number of segments
   int64_t units, slots;   // room in meta and in part
-  int M;             // rows of a tile
+  int M, shift;      // rows of a tile: a power of two, and its logarithm
 };
 
 struct AttendArgs {
