@@ -22,6 +22,19 @@ constexpr int kThreadsA = 256;
 __device__ __forceinline__ float2 two(uint32_t w) {
   return make_float2(sv_lo(w), sv_hi(w));
 }
+// Products by pairs, sums one by one: with sums by pairs too, some of them
+// come out fused with a product into one rounding (as instructions, as
+// intrinsics, and as multiply-adds by 1), which is not what the decode step
+// computes.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  return __fmul2_rn(a, b);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  return make_float2(__fsub_rn(a.x, b.x), __fsub_rn(a.y, b.y));
+}
 __device__ __forceinline__ uint32_t pack2(float2 v) {
   return sv_pack(v.x, v.y);
 }
@@ -138,13 +151,12 @@ __global__ void __launch_bounds__(kThreadsA, 2)
       const float2 rr = make_float2(r, r);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[i] = two(pack2(__fmul2_rn(__fmul2_rn(x[i], rr), two(words(wa)[i]))));
-        y[i] = two(pack2(__fmul2_rn(__fmul2_rn(y[i], rr), two(words(wb)[i]))));
+        x[i] = two(pack2(mul2(mul2(x[i], rr), two(words(wa)[i]))));
+        y[i] = two(pack2(mul2(mul2(y[i], rr), two(words(wb)[i]))));
       }
     }
     const bool rot = turns && (isq || isk);
     if (rot) {
-      const float2 m1 = make_float2(-1.f, -1.f);
       if (a.interleaved) {
         // pairs lie side by side: (even, odd) of two values to (evens, odds)
 #pragma unroll
@@ -153,10 +165,9 @@ __global__ void __launch_bounds__(kThreadsA, 2)
           const float2 e = make_float2(z[0].x, z[1].x);
           const float2 o = make_float2(z[0].y, z[1].y);
           const float2 q =
-              __fadd2_rn(__fmul2_rn(e, cs[i]),
-                         __fmul2_rn(m1, __fmul2_rn(o, sn[i])));
+              sub2(mul2(e, cs[i]), mul2(o, sn[i]));
           const float2 w =
-              __fadd2_rn(__fmul2_rn(o, cs[i]), __fmul2_rn(e, sn[i]));
+              add2(mul2(o, cs[i]), mul2(e, sn[i]));
           z[0] = make_float2(q.x, w.x);
           z[1] = make_float2(q.y, w.y);
         }
@@ -164,9 +175,8 @@ __global__ void __launch_bounds__(kThreadsA, 2)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 e = x[i], o = y[i];
-          x[i] = __fadd2_rn(__fmul2_rn(e, cs[i]),
-                            __fmul2_rn(m1, __fmul2_rn(o, sn[i])));
-          y[i] = __fadd2_rn(__fmul2_rn(o, cs[i]), __fmul2_rn(e, sn[i]));
+          x[i] = sub2(mul2(e, cs[i]), mul2(o, sn[i]));
+          y[i] = add2(mul2(o, cs[i]), mul2(e, sn[i]));
         }
       }
     }

@@ -689,6 +689,27 @@ def test_append_values_keep_their_bits():
 
 
 @gpu
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_append_rotation_rounds_each_operation(inter, d):
+    # products and the sum of a pair are fp32 operations of their own, as in
+    # the decode step: the result is the same to the last bit
+    c, qkv, rot, qn, kn, k0, v0, qo = _append_case(25, n=[40, 7], ctx=[9, 200],
+                                                   inter=inter, d=d)
+    pos = np.array([9 + i for i in range(40)] + [200 + i for i in range(7)])
+    table = mpk.mpk_rope_table(d, 240, 1e4).cpu().numpy()[pos]
+    x = qkv[:, :c.hq * d].float().cpu().numpy().reshape(-1, c.hq, d)
+    cs, sn = table[:, None, :, 0], table[:, None, :, 1]
+    a, b = (x[..., 0::2], x[..., 1::2]) if inter else (x[..., :d // 2],
+                                                       x[..., d // 2:])
+    lo, hi = a * cs - b * sn, b * cs + a * sn       # numpy: no fusing
+    y = (np.stack([lo, hi], -1).reshape(x.shape) if inter else
+         np.concatenate([lo, hi], -1))
+    want = torch.from_numpy(y).bfloat16().reshape(-1, c.hq * d)
+    assert torch.equal(qo.cpu(), want)
+
+
+@gpu
 def test_append_in_place_and_separate_tensors():
     c, qkv, rot, qn, kn, k0, v0, qo = _append_case(23, n=[2, 5], ctx=[6, 1],
                                                    norm=True)
