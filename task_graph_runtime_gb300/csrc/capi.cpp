@@ -8,6 +8,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <memory>
+#include <mutex>
 #include <new>
 #include <string>
 #include <vector>
@@ -22,6 +23,19 @@
 using namespace mpk;
 
 using namespace mpk_detail;
+
+cudaError_t mpk::raise_smem_limit(int smem) {
+  static std::mutex mu;
+  static int largest[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev < 64 && smem <= largest[dev]) return cudaSuccess;
+  e = configure_kernels(smem);
+  if (e == cudaSuccess && dev < 64) largest[dev] = smem;
+  return e;
+}
 
 namespace {
 
@@ -318,7 +332,7 @@ mpk_status mpk_bind_weights(mpk_graph* g, const mpk_weights* w) {
   if (!smem_layout(g->bg, g->pages_req, std::min(optin, kSmemLimit), &sm))
     return MPK_ERR_UNSUPPORTED;
   g->smem = sm.total;
-  CK(configure_kernels(g->smem));
+  CK(raise_smem_limit(g->smem));
   if (megakernel_max_blocks_per_sm(g->smem) < 1) return MPK_ERR_NOT_CORESIDENT;
   g->device = dev;
 
@@ -364,6 +378,7 @@ mpk_status mpk_bind_weights(mpk_graph* g, const mpk_weights* w) {
       ptrs[(size_t)l * MPK_LAYER_NTENSORS + k] = static_cast<const uint16_t*>(
           w->layers[(size_t)l * MPK_LAYER_NTENSORS + k]);
   CK(g->d_layer_ptrs.upload(ptrs));
+  g->h_layer_ptrs = ptrs;
 
   KernelParams& P = g->params;
   P = KernelParams{};

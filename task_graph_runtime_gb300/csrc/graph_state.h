@@ -68,6 +68,7 @@ struct mpk_graph {
   DevBuf<uint64_t> d_jit_slots, d_sched_slots;
   DevBuf<char> d_act;
   DevBuf<const uint16_t*> d_layer_ptrs;
+  std::vector<const uint16_t*> h_layer_ptrs;   // [L][MPK_LAYER_NTENSORS]
   DevBuf<float> d_rope;
   DevBuf<uint64_t> d_trace;
   DevBuf<uint32_t> d_trace_count;

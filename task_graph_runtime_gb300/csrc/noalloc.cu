@@ -127,7 +127,7 @@ extern "C" mpk_status mpk_decode_step_noalloc(
                                                   : mpk_detail::kSmemLimit,
                    &sm))
     return MPK_ERR_UNSUPPORTED;
-  if (configure_kernels(sm.total) != cudaSuccess) return MPK_ERR_CUDA;
+  if (raise_smem_limit(sm.total) != cudaSuccess) return MPK_ERR_CUDA;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
 
   // --- fill the scratch array.  The status words and the merge counters
