@@ -548,6 +548,33 @@ mpk_status mpk_verify_drafts(const mpk_token_batch* tok,
                              size_t workspace_bytes, uint32_t* d_status,
                              void* cuda_stream);
 
+/* One step of drafted decoding of a whole model: the graph's rows are the
+ * rows of *tok (so n_tokens is the batch that the graph was built for, and
+ * tok->batch, at most as many, is the number of sequences), a sequence's
+ * rows being its last accepted token and its drafts.  Runs the graph's
+ * kernel-per-operator form (whatever its mode) with mpk_kv_append and
+ * mpk_prefix_attention in the place of its attention, and mpk_verify_drafts
+ * on the logits in the place of its argmax.  With one row a sequence, no
+ * draft and T <= 0 it is mpk_decode_step over prefixes that are read once.
+ *   v->tokens        the rows' input tokens, all in [0, vocab), those of
+ *                    padding rows too
+ *   v->logits        ignored, as are v->vocab, v->logits_stride and
+ *                    v->seq_lens: the step's own (d_logits, fp32
+ *                    [n_tokens][vocab], and kv->seq_lens)
+ *   v->seq_lens_out  kv->seq_lens to keep the accepted tokens' keys and
+ *                    values (those of the refused ones are overwritten by
+ *                    the next step), null to leave the lengths alone
+ * groups may be null.  Errors found on the device are those of the three
+ * calls, in the graph's status word (mpk_get_status, mpk_reset).
+ * MPK_ERR_UNSUPPORTED for the chained-linear mode. */
+size_t mpk_verify_step_workspace(const mpk_graph* g,
+                                 const mpk_token_batch* tok, int n_groups);
+mpk_status mpk_verify_step(mpk_graph* g, const mpk_token_batch* tok,
+                           const mpk_prefix_groups* groups,
+                           const mpk_kv_cache* kv, const mpk_verify_args* v,
+                           float* d_logits, void* d_workspace,
+                           size_t workspace_bytes, void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -4,6 +4,8 @@
 
 #include <cmath>
 
+#include "graph_state.h"
+#include "launch.h"
 #include "mpk.h"
 #include "serve.h"
 
@@ -242,10 +244,9 @@ size_t mpk_verify_drafts_workspace(const mpk_token_batch* tok, int vocab) {
   return verify_workspace(&a, nullptr);
 }
 
-mpk_status mpk_verify_drafts(const mpk_token_batch* tok,
-                             const mpk_verify_args* v, void* d_workspace,
-                             size_t workspace_bytes, uint32_t* d_status,
-                             void* cuda_stream) {
+static mpk_status check_verify(const mpk_token_batch* tok,
+                               const mpk_verify_args* v,
+                               const uint32_t* d_status) {
   mpk_status st = check_batch(tok);
   if (st != MPK_OK) return st;
   const bool none = tok->n_tokens == 0;   // outputs alone are written
@@ -262,6 +263,15 @@ mpk_status mpk_verify_drafts(const mpk_token_batch* tok,
     return MPK_ERR_UNSUPPORTED;
   if (!tok->q_start && tok->tokens_per_seq > v->max_out)
     return MPK_ERR_INVALID_ARG;
+  return MPK_OK;
+}
+
+mpk_status mpk_verify_drafts(const mpk_token_batch* tok,
+                             const mpk_verify_args* v, void* d_workspace,
+                             size_t workspace_bytes, uint32_t* d_status,
+                             void* cuda_stream) {
+  const mpk_status st = check_verify(tok, v, d_status);
+  if (st != MPK_OK) return st;
   VerifyArgs a{};
   a.batch = tok->batch;
   a.n_tokens = tok->n_tokens;
@@ -290,6 +300,100 @@ mpk_status mpk_verify_drafts(const mpk_token_batch* tok,
   a.seq_lens_out = v->seq_lens_out;
   a.status = d_status;
   return from_cuda(launch_verify(a, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+// The graph's heads and cache geometry.
+static mpk_attn_shape graph_shape(const mpk_graph* g) {
+  const mpk_model_shape& s = g->bg.cfg.shape;
+  return mpk_attn_shape{s.n_q_heads, s.n_kv_heads, s.head_dim, s.page_size,
+                        s.max_pages_per_seq};
+}
+
+size_t mpk_verify_step_workspace(const mpk_graph* g,
+                                 const mpk_token_batch* tok, int n_groups) {
+  if (!g || !tok || g->bg.cfg.shape.chain_ffn > 0 ||
+      tok->n_tokens != g->bg.cfg.batch)
+    return 0;
+  // the attention's workspace is free again when the drafts are judged
+  const mpk_attn_shape s = graph_shape(g);
+  const size_t a = mpk_prefix_attention_workspace(&s, tok, n_groups);
+  const size_t b = mpk_verify_drafts_workspace(tok, g->bg.cfg.shape.vocab);
+  return a == 0 || b == 0 ? 0 : a > b ? a : b;
+}
+
+mpk_status mpk_verify_step(mpk_graph* g, const mpk_token_batch* tok,
+                           const mpk_prefix_groups* groups,
+                           const mpk_kv_cache* kv, const mpk_verify_args* v,
+                           float* d_logits, void* d_workspace,
+                           size_t workspace_bytes, void* cuda_stream) {
+  if (!g || !v || !d_logits || !v->tokens) return MPK_ERR_INVALID_ARG;
+  if (!g->bound) return MPK_ERR_NOT_BOUND;
+  const mpk_model_shape& s = g->bg.cfg.shape;
+  if (s.chain_ffn > 0) return MPK_ERR_UNSUPPORTED;
+  const mpk_attn_shape shape = graph_shape(g);
+  mpk_status st = check_batch(tok);
+  if (st != MPK_OK) return st;
+  if (tok->n_tokens != g->bg.cfg.batch || tok->batch > tok->n_tokens)
+    return MPK_ERR_INVALID_ARG;
+  uint32_t* status = g->d_status.p;
+  PagedArgs probe{};                    // what the launches below would refuse
+  st = fill_paged(&shape, tok, kv, 0, status, &probe);
+  if (st != MPK_OK) return st;
+  const size_t need =
+      mpk_verify_step_workspace(g, tok, groups ? groups->n_groups : 0);
+  if (need == 0 || !d_workspace || off(d_workspace, 256) ||
+      workspace_bytes < need)
+    return MPK_ERR_INVALID_ARG;
+  mpk_verify_args judge = *v;
+  judge.vocab = s.vocab;
+  judge.logits = d_logits;
+  judge.logits_stride = s.vocab;
+  judge.seq_lens = kv->seq_lens;
+  st = check_verify(tok, &judge, status);
+  if (st != MPK_OK) return st;
+  if (cudaSetDevice(g->device) != cudaSuccess) return MPK_ERR_CUDA;
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  KernelParams P = g->params;
+  StepArgs a{};
+  a.tokens = v->tokens;
+  a.logits = d_logits;
+  a.timeout_ns = g->timeout_ns;
+  a.n_steps = 1;
+  a.k_pool = static_cast<uint16_t*>(kv->k_pool);
+  a.v_pool = static_cast<uint16_t*>(kv->v_pool);
+  a.page_table = kv->page_table;
+  a.seq_lens = kv->seq_lens;
+  a.num_pages = kv->num_pages;
+  a.epoch = g->epoch;
+  P.step = a;
+  const int64_t wq = (int64_t)s.n_q_heads * s.head_dim,
+                wk = (int64_t)s.n_kv_heads * s.head_dim, row = wq + 2 * wk;
+  const mpk_rope rope{g->d_rope.p, P.dims.max_ctx, s.head_dim, 0};
+  for (size_t o = 0; o < g->bg.ops.size(); ++o) {
+    const BOp& op = g->bg.ops[o];
+    if (op.kind == MPK_TASK_ARGMAX) continue;
+    if (op.kind != MPK_TASK_ATTN) {
+      const cudaError_t e =
+          launch_kpo_op(P, g->h_op_first[o], op.n, g->smem, stream);
+      if (e != cudaSuccess) return from_cuda(e);
+      continue;
+    }
+    char* layer = P.act.base + (int64_t)op.layer * P.act.layer_stride;
+    uint16_t* q = reinterpret_cast<uint16_t*>(layer + P.act.o_qkv);
+    const uint16_t* const* w =
+        g->h_layer_ptrs.data() + (size_t)op.layer * MPK_LAYER_NTENSORS;
+    st = mpk_kv_append(&shape, tok, kv, op.layer, q, row, q + wq, row,
+                       q + wq + wk, row, s.qk_norm ? w[MPK_W_QNORM] : nullptr,
+                       s.qk_norm ? w[MPK_W_KNORM] : nullptr, s.rms_eps, &rope,
+                       q, row, status, cuda_stream);
+    if (st != MPK_OK) return st;
+    st = mpk_prefix_attention(&shape, tok, groups, kv, op.layer, q, row, 0.f,
+                              layer + P.act.o_attn, wq, nullptr, d_workspace,
+                              workspace_bytes, status, cuda_stream);
+    if (st != MPK_OK) return st;
+  }
+  return mpk_verify_drafts(tok, &judge, d_workspace, workspace_bytes, status,
+                           cuda_stream);
 }
 
 }  // extern "C"

@@ -204,6 +204,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                   ctypes.c_size_t, vp, vp], st),
         "mpk_verify_drafts_workspace": ([ctypes.POINTER(TokenBatch), i],
                                         ctypes.c_size_t),
+        "mpk_verify_step_workspace": ([vp, ctypes.POINTER(TokenBatch), i],
+                                      ctypes.c_size_t),
+        "mpk_verify_step": ([vp, ctypes.POINTER(TokenBatch),
+                             ctypes.POINTER(PrefixGroups),
+                             ctypes.POINTER(_KVCache),
+                             ctypes.POINTER(VerifyArgs), vp, vp,
+                             ctypes.c_size_t, vp], st),
         "mpk_verify_drafts": ([ctypes.POINTER(TokenBatch),
                                ctypes.POINTER(VerifyArgs), vp,
                                ctypes.c_size_t, vp, vp], st),
@@ -334,6 +341,7 @@ class Graph:
                                coarse_events)
         self.handle = mpk_build_tgraph(self.c_shape, self.tiles, batch)
         self._keep = None
+        self._ws = None            # verify_step's
 
     def export(self) -> Dict[str, np.ndarray]:
         return mpk_export_tgraph(self.handle)
@@ -382,6 +390,90 @@ class Graph:
             ctypes.byref(kvs) if kvs is not None else None,
             logits.data_ptr(), next_tokens.data_ptr(), n_steps, s),
             "mpk_decode_steps")
+
+    def verify_step(self, tokens, kv: KVCache, logits, uniform, noise,
+                    n_accepted, out_tokens, q_start=None, group_start=None,
+                    prefix_len=None, draft=None, draft_is_logits=False,
+                    temperature=None, logprobs=None, next_tokens=None,
+                    advance: bool = True, stream=None):
+        """One step of drafted decoding (mpk_verify_step): this graph's batch
+        is the number of rows, the page table's rows are the sequences.
+        Arguments as for ``DraftVerifier.verify`` and ``PagedBatch``;
+        ``advance`` moves kv.seq_lens past the accepted tokens.  The workspace
+        is the graph's own and grows with the first call of a shape."""
+        import torch
+        w = "Graph.verify_step"
+        lib, i32, f32 = load_library(), torch.int32, torch.float32
+        dev = _OnDevice()
+        dev._on(_cuda_device(kv.page_table, w))
+        rows, V = self.batch, self.shape.vocab
+        B = int(kv.page_table.shape[0])
+        if out_tokens.dim() != 2 or B < 1 or B > rows:
+            _refuse(w, "out_tokens must be [sequences, max_out], and the "
+                       "sequences no more than the graph's batch")
+        if q_start is None and rows % B:
+            _refuse(w, "the graph's batch must be a multiple of the "
+                       "sequences without q_start")
+        if tuple(kv.page_table.shape) != (
+                B, self.c_shape.max_pages_per_seq):
+            _refuse(w, "page_table must be [sequences, max_pages_per_seq]")
+        want = (self.shape.n_layers, self.shape.n_kv_heads,
+                self.c_shape.page_size, self.shape.head_dim)
+        for pool in (kv.k_pool, kv.v_pool):
+            if (pool.dtype is not torch.bfloat16 or pool.dim() != 5 or
+                    not pool.is_contiguous() or
+                    pool.get_device() != dev._index or
+                    (pool.shape[0], *pool.shape[2:]) != want or
+                    pool.shape != kv.k_pool.shape):
+                _refuse(w, "k_pool and v_pool must be the graph's")
+        mo = int(out_tokens.shape[1])
+        vec = dev._vec
+        vec(kv.page_table, 0, i32, w, "page_table")
+        seq = vec(kv.seq_lens, B, i32, w, "seq_lens")
+        tok = TokenBatch(B, rows, vec(q_start, B + 1, i32, w, "q_start"),
+                         rows // B)
+        groups = None
+        if (group_start is None) != (prefix_len is None):
+            _refuse(w, "group_start and prefix_len come together")
+        if prefix_len is not None:
+            n = int(prefix_len.numel())
+            groups = PrefixGroups(
+                n, vec(group_start, n + 1, i32, w, "group_start"),
+                vec(prefix_len, n, i32, w, "prefix_len"))
+
+        def matrix(t, n, name):
+            if t is None:
+                return None, 0
+            if (t.dtype is not f32 or t.get_device() != dev._index or
+                    t.dim() != 2 or t.shape[0] < n or t.shape[1] != V or
+                    (V > 1 and t.stride(1) != 1)):
+                _refuse(w, f"{name} must be float32 [{n}, {V}]")
+            return t.data_ptr(), (t.stride(0) if n > 1 else V)
+        dp, ds = matrix(draft, rows, "draft")
+        np_, ns = matrix(noise, B, "noise")
+        a = VerifyArgs(
+            vocab=V, max_out=mo, tokens=vec(tokens, rows, i32, w, "tokens"),
+            draft=dp, draft_stride=ds, draft_is_logits=int(draft_is_logits),
+            temperature=vec(temperature, B, f32, w, "temperature"),
+            uniform=vec(uniform, rows, f32, w, "uniform"), noise=np_,
+            noise_stride=ns,
+            n_accepted=vec(n_accepted, B, i32, w, "n_accepted"),
+            out_tokens=vec(out_tokens, B * mo, i32, w, "out_tokens"),
+            logprobs=vec(logprobs, B * mo, f32, w, "logprobs"),
+            next_tokens=vec(next_tokens, B, i32, w, "next_tokens"),
+            seq_lens_out=seq if advance else None)
+        lg = vec(logits, rows * V, f32, w, "logits")
+        need = lib.mpk_verify_step_workspace(
+            self.handle, ctypes.byref(tok), groups.n_groups if groups else 0)
+        if self._ws is None or self._ws.numel() < need:
+            self._ws = torch.empty(max(need, 1), dtype=torch.uint8,
+                                   device=dev.device)
+        kvs = kv.c_struct()
+        _check(dev._call(
+            lib.mpk_verify_step, self.handle, ctypes.byref(tok),
+            ctypes.byref(groups) if groups else None, ctypes.byref(kvs),
+            ctypes.byref(a), lg, self._ws.data_ptr(), self._ws.numel(),
+            dev._stream(stream)), "mpk_verify_step")
 
     def status(self) -> int:
         return load_library().mpk_get_status(self.handle)
