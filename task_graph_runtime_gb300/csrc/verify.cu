@@ -294,7 +294,8 @@ __device__ __noinline__ unsigned long long race_plain(const Race& r,
 // 3 p without one token.  VEC: the rows lie on the same 16-byte phase.
 template <int KIND, bool VEC>
 __device__ __forceinline__ unsigned long long race_slice(const Race& r,
-                                                         int vocab) {
+                                                         int vocab,
+                                                         int* s_floor) {
   const int tid = threadIdx.x;
   constexpr bool Q = KIND == 1 || KIND == 2;
   constexpr int U = 4;                 // vectors of four a turn
@@ -304,7 +305,9 @@ __device__ __forceinline__ unsigned long long race_slice(const Race& r,
   const int v1 = (int)((int64_t)nv * (blockIdx.x + 1) / gridDim.x);
   unsigned long long best = 0ull;
   float floor_ = 0.f;                  // the best is at least this
+  // (as bits: positive floats order as whole numbers)
   for (int v = v0; v < v1; v += U * kNT) {
+    floor_ = fmaxf(floor_, __int_as_float(*(volatile int*)s_floor));
     float up[4 * U];
     float low = 0.f;
     // value j of vector i: 4 (v + i kNT + tid) - o + j, or without a common
@@ -357,7 +360,11 @@ __device__ __forceinline__ unsigned long long race_slice(const Race& r,
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1)
       low = fmaxf(low, __shfl_xor_sync(0xffffffffu, low, s));
-    floor_ = fmaxf(floor_, low);
+    if (low > floor_) {
+      // the other warps have less to work out next turn
+      floor_ = low;
+      if ((tid & 31) == 0) atomicMax(s_floor, __float_as_int(low));
+    }
     uint32_t mask = 0;
 #pragma unroll
     for (int i = 0; i < 4 * U; ++i)
@@ -381,6 +388,7 @@ __global__ void __launch_bounds__(kNT)
   __shared__ VerifyRow s_row[2][kMaxOut];
   __shared__ int s_stop;       // first draft that is not accepted
   __shared__ int s_last;
+  __shared__ int s_floor;      // a lower bound of the slice's best, as bits
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   // (verify_stats has waited for what comes before it)
   RowInfo r = rows_of(a, b);
@@ -395,7 +403,10 @@ __global__ void __launch_bounds__(kNT)
   // log2(e) / T in two parts
   const float ch = greedy ? 1.f : kLog2e / T;
   const float cl = greedy ? 0.f : (fmaf(-ch, T, kLog2e) + kLog2eLow) / T;
-  if (tid == 0) s_stop = r.n - 1;
+  if (tid == 0) {
+    s_stop = r.n - 1;
+    s_floor = 0;
+  }
   // the rows' slices, a warp a row; lane 0 has what judges the draft ready
   bool waited = false;
   for (int i = tid >> 5; i < r.n; i += kNT / 32) {
@@ -483,14 +494,14 @@ __global__ void __launch_bounds__(kNT)
       const bool same = (((uintptr_t)g.e >> 2) & 3) == o &&
                         (!g.y || (((uintptr_t)g.y >> 2) & 3) == o);
       if (g.y && dlog)
-        best = same ? race_slice<2, true>(g, a.vocab)
-                    : race_slice<2, false>(g, a.vocab);
+        best = same ? race_slice<2, true>(g, a.vocab, &s_floor)
+                    : race_slice<2, false>(g, a.vocab, &s_floor);
       else if (g.y)
-        best = same ? race_slice<1, true>(g, a.vocab)
-                    : race_slice<1, false>(g, a.vocab);
+        best = same ? race_slice<1, true>(g, a.vocab, &s_floor)
+                    : race_slice<1, false>(g, a.vocab, &s_floor);
       else
-        best = same ? race_slice<3, true>(g, a.vocab)
-                    : race_slice<3, false>(g, a.vocab);
+        best = same ? race_slice<3, true>(g, a.vocab, &s_floor)
+                    : race_slice<3, false>(g, a.vocab, &s_floor);
     }
     if (lane == 0 && best) atomicMax(a.race + b, best);
   }
@@ -570,10 +581,11 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
   cudaError_t e = sv_launch(verify_stats, dim3(a.slices, rows, dlog ? 2 : 1),
                             kNT, 0, s, a);
   if (e != cudaSuccess) return e;
-  // slices of a race: the same rule, 4096 values (one turn) at least
-  int64_t n = (152 * 4 + a.batch - 1) / a.batch;
-  const int64_t hi = (a.vocab + 4095) / 4096;
-  n = n > hi ? hi : n;
+  // Slices of a race: whole turns of 4096 values a CTA, as few as keep the
+  // grid within one wave of three CTAs an SM.
+  const int64_t turns = ((int64_t)a.vocab + 4095) / 4096;
+  const int64_t each = (turns * a.batch + 152 * 3 - 1) / (152 * 3);
+  const int64_t n = (turns + each - 1) / each;
   return sv_launch(verify_sample, dim3((unsigned)n, a.batch), kNT, 0, s, a);
 }
 
