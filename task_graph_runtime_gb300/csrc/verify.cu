@@ -69,7 +69,7 @@ __device__ __forceinline__ RowInfo rows_of(const VerifyArgs& a, int b) {
   return r;
 }
 
-__global__ void __launch_bounds__(kNT)
+__global__ void __launch_bounds__(kNT, 5)
     verify_stats(const __grid_constant__ VerifyArgs a) {
   sv_grid_wait();
   sv_grid_launch();
@@ -406,6 +406,15 @@ __global__ void __launch_bounds__(kNT)
   if (tid == 0) {
     s_stop = r.n - 1;
     s_floor = 0;
+  }
+  // The slice's noise does not depend on the verdicts: into the L2 while the
+  // first pass drains.
+  if (!greedy) {
+    const float* e = a.noise + b * a.noise_stride;
+    const int e0 = (int)((int64_t)a.vocab * blockIdx.x / gridDim.x);
+    const int e1 = (int)((int64_t)a.vocab * (blockIdx.x + 1) / gridDim.x);
+    for (int k = e0 + 32 * tid; k < e1; k += 32 * kNT)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(e + k));
   }
   // the rows' slices, a warp a row; lane 0 has what judges the draft ready
   bool waited = false;
