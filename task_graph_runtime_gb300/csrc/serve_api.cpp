@@ -277,6 +277,8 @@ mpk_status mpk_verify_drafts(const mpk_token_batch* tok,
   a.n_tokens = tok->n_tokens;
   a.vocab = v->vocab;
   a.max_out = v->max_out;
+  a.draft = v->draft;
+  a.draft_is_logits = v->draft_is_logits;
   a.q_start = tok->q_start;
   a.tokens_per_seq = tok->tokens_per_seq;
   if (!d_workspace || off(d_workspace, 256) ||

@@ -16,12 +16,15 @@
 // of CTAs took half as long again as leaving them to the second pass).
 // verify_sample: every CTA of a sequence joins its rows' slices (a warp a
 // row; in fp32: the FP64 units are few, and 64-bit sums here cost 10 us a
-// launch), finds the first refused draft and races its slice of that one row; slices meet in one 64-bit atomic maximum of
+// launch), finds the first refused draft and races its slice of that one row;
+// slices meet in one 64-bit atomic maximum of
 // (value, lowest index), whose result does not depend on their order.  Most
 // values of a slice cannot win: bounds from fast functions decide that, and
 // only the few above a warp's best lower bound are worked out exactly.
 // Bound by HBM: each row of logits leaves it once, the row that is sampled
 // from once more with its draft and noise rows.
+#include <cmath>
+
 #include "serve_dev.cuh"
 
 namespace mpk {
@@ -558,13 +561,23 @@ __global__ void __launch_bounds__(kNT)
   }
 }
 
-// Slices of a row in the first pass: at most 16384 values, fewer when there
-// are few rows (about four CTAs an SM), 2048 at least.
-int row_slices(const VerifyArgs& a) {
-  const int64_t rows = a.n_tokens > 0 ? a.n_tokens : 1;
-  int64_t s = (152 * 4 + rows - 1) / rows;
-  const int64_t lo = (a.vocab + 16383) / 16384, hi = (a.vocab + 2047) / 2048;
-  return (int)(s < lo ? lo : s > hi ? hi : s);
+// Slices of a row in the first pass: those with the shortest time by waves of
+// five CTAs an SM, each with 1.5 us to find out what its row is and its share
+// of the 5.7 TB/s that such a wave reads (measured); 2048 values at least.
+// (384 rows of 151936: 10 slices, 5.05 waves, took 49 us.)
+int row_slices(const VerifyArgs& a, int64_t rows) {
+  const double wave = 152 * 5, row_us = a.vocab * 4.0 * wave / 5.7e6;
+  const int hi = (a.vocab + 2047) / 2048;
+  int best = 1;
+  double least = 1e30;
+  for (int s = 1; s <= hi && s <= 128; ++s) {
+    const double us = std::ceil(rows * s / wave) * (1.5 + row_us / s);
+    if (us < least) {
+      least = us;
+      best = s;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -577,8 +590,12 @@ size_t verify_workspace(VerifyArgs* a, char* base) {
     return p;
   };
   const size_t rows = a->n_tokens > 0 ? a->n_tokens : 1;
-  a->slices = row_slices(*a);
-  a->part = reinterpret_cast<float4*>(take(2 * rows * a->slices * 16));
+  // (a call without drafts' logits has half the rows, and may have up to
+  // twice the slices: room for either)
+  const int one = row_slices(*a, rows), both = row_slices(*a, 2 * rows);
+  a->slices = a->draft && a->draft_is_logits ? both : one;
+  a->part = reinterpret_cast<float4*>(
+      take(rows * (size_t)(one > 2 * both ? one : 2 * both) * 16));
   a->race = reinterpret_cast<unsigned long long*>(take((size_t)a->batch * 8));
   a->arrived = reinterpret_cast<uint32_t*>(take((size_t)a->batch * 4));
   return off;
