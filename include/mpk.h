@@ -377,7 +377,9 @@ mpk_status mpk_decode_step_noalloc(const mpk_graph* g, const mpk_weights* w,
  * arguments' is touched. */
 
 /* Heads of one layer and the geometry of its cache (mpk_kv_cache layout).
- * head_dim is 32, 64 or 128; n_q_heads a multiple of n_kv_heads. */
+ * head_dim is 32, 64 or 128; n_q_heads a multiple of n_kv_heads; page_size
+ * times max_pages_per_seq at most 2^30; the pools' num_pages x n_kv_heads x
+ * page_size rows of a layer fewer than 2^32. */
 typedef struct {
   int n_q_heads;
   int n_kv_heads;
@@ -509,7 +511,8 @@ mpk_status mpk_prefix_attention(const mpk_attn_shape* shape,
  * argmax_v max(p_v - q_v, 0) / noise[b][v] (p alone where that is nowhere
  * positive; without `draft`, p without the refused token), and with all
  * accepted argmax_v p_v / noise[b][v] of the last row; ties take the lowest
- * index.  With uniform in [0, 1) and noise ~ Exp(1), the emitted tokens are
+ * index.  Outputs overlap no inputs, but for seq_lens_out.  With uniform in
+ * [0, 1) and noise ~ Exp(1), the emitted tokens are
  * distributed as samples of p.  T <= 0 is greedy: a draft is accepted when it
  * is the row's argmax, the next token is the argmax.  NaN logits count as
  * -inf, several +inf share the row; a row of nothing but -inf accepts nothing

@@ -22,11 +22,17 @@
 // A fifth warp walks the stretch ahead of them: it looks up the pages (one
 // block early), copies K, V and the queries of a 16-row tile into a ring of
 // kStages shared-memory stages, and leaves a description of the block there.
-// Pages that are a multiple of 8 tokens come as TMA boxes, others key by key
-// in 16-byte copies (one warp's 64 such instructions a block took longer than
-// the block: 66 us instead of CHECK at 256 sequences of 1..512 own keys).  The others touch no list, table or length, and a stretch of many
-// short sequences streams like one long one: the chain lengths -> pages ->
-// keys that starts a sequence runs while earlier blocks are computed.
+// Pages that are a multiple of 8 tokens come as TMA boxes (blocks begin at
+// multiples of 64 keys, so that boxes do not cross pages), others key by key
+// in 16-byte copies; the computing warps clear the values of keys outside the
+// entity's.  They touch no list, table or length, and a stretch of many short
+// sequences streams like one long one: the chain lengths -> pages -> keys that
+// starts a sequence runs while earlier blocks are computed.
+//
+// Measured (head_dim 128, 32 / 8 heads): 256 sequences with 1..512 own keys,
+// 269 MB, 53 us = 5.1 TB/s; 16 sequences of 1..2048 own keys behind a prefix
+// of 2048, 79 MB, 22 us: there 5 us go into the plan and the first block's
+// way, and 1100 to 1700 cycles a block are the chain of its instructions.
 #pragma once
 
 #include "attend_plan.cuh"
@@ -256,8 +262,9 @@ struct Copier {
       const bool stop = d.unit >= set.units;
       end = c.pos + (prefix ? W : 1) >= ps.x1;
       const bool last = c.blk + 1 == c.nb || end;
-      d.flags = (end ? BLK_END : 0) | (prefix ? BLK_PREFIX : 0) | (first ? BLK_FIRST : 0) |
-                (last ? BLK_LAST : 0) | (stop ? BLK_STOP : 0);
+      d.flags = (end ? BLK_END : 0) | (prefix ? BLK_PREFIX : 0) |
+                (first ? BLK_FIRST : 0) | (last ? BLK_LAST : 0) |
+                (stop ? BLK_STOP : 0);
       // rows of the pool (32-bit numbers: 2^32 rows of 64 bytes are more
       // than the memory)
       uint32_t row[2];
@@ -345,6 +352,7 @@ struct Copier {
       }
       if (stop) {   // q_start or group_start not ascending
         sv_latch(p.status, MPK_ERR_INVALID_ARG);
+        ++sent;
         break;
       }
       first = last;
@@ -409,27 +417,25 @@ struct Attend {
       for (int k = 0; k < D / 16; ++k)
         ldm4(q + swz<D, 16>(lane & 15, 2 * k + (lane >> 4)), qf[k]);
     } else {
-    const PagedArgs& p = a.p;
-    const int wm = (threadIdx.x >> 5) % WM;
-    const int grp = p.Hq / p.Hkv;
+      const PagedArgs& p = a.p;
+      const int wm = (threadIdx.x >> 5) % WM, grp = p.Hq / p.Hkv;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = b.tile * 16 * WM + wm * 16 + (lane >> 2) + 8 * r;
-      const bool ok = row < b.rows;
-      const int tok = ok ? row / grp : 0;
-      const uint16_t* src = a.q + (b.tok0 + tok) * a.q_stride +
-                            (int64_t)(b.h * grp + (ok ? row - tok * grp : 0)) *
-                                D +
-                            2 * (lane & 3);
+      for (int r = 0; r < 2; ++r) {
+        const int row = b.tile * 16 * WM + wm * 16 + (lane >> 2) + 8 * r;
+        const bool ok = row < b.rows;
+        const int tok = ok ? (int)sv_div(row, p.grp_div) : 0;
+        const int j = ok ? row - tok * grp : 0;
+        const uint16_t* src = a.q + (b.tok0 + tok) * a.q_stride +
+                              (int64_t)(b.h * grp + j) * D + 2 * (lane & 3);
+        auto word = [&](int c) {
+          return ok ? __ldg(reinterpret_cast<const uint32_t*>(src + c)) : 0u;
+        };
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        qf[k][r] = ok ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k))
-                      : 0u;
-        qf[k][2 + r] =
-            ok ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 8))
-               : 0u;
+        for (int k = 0; k < D / 16; ++k) {
+          qf[k][r] = word(16 * k);
+          qf[k][2 + r] = word(16 * k + 8);
+        }
       }
-    }
     }
   }
 

@@ -134,8 +134,14 @@ __device__ __forceinline__ Ent att_seq_ent(const AttendArgs& a, int b) {
   const int n =
       max(sv_row(p.q_start, p.tokens_per_seq, p.n_tokens, b + 1) - e.tok0, 0);
   e.rows = n * (p.Hq / p.Hkv);
-  const int len = __ldg(p.seq_lens + b);
-  e.k0 = att_prefix(a, att_group(a, b));
+  const int len = __ldg(p.seq_lens + b), g = att_group(a, b);
+  e.k0 = att_prefix(a, g);
+  if (a.n_groups > 0 && (__ldg(a.group_start + g) > b ||
+                         __ldg(a.group_start + g + 1) <= b)) {
+    // in no group: the groups do not go from 0 to the batch
+    if (n > 0) sv_latch(p.status, MPK_ERR_INVALID_ARG);
+    e.k0 = 0;
+  }
   const int64_t end = (int64_t)len + n;
   const int ctx = att_ctx(p);
   e.k1 = end > ctx ? ctx : (int)end;

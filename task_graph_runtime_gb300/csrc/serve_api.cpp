@@ -32,8 +32,8 @@ mpk_status check_shape(const mpk_attn_shape* s) {
     return MPK_ERR_INVALID_ARG;
   if (s->head_dim != 32 && s->head_dim != 64 && s->head_dim != 128)
     return MPK_ERR_UNSUPPORTED;
-  if ((int64_t)s->page_size * s->max_pages_per_seq > 0x7fffffff)
-    return MPK_ERR_UNSUPPORTED;
+  if ((int64_t)s->page_size * s->max_pages_per_seq > 0x40000000)
+    return MPK_ERR_UNSUPPORTED;         // positions are 32-bit numbers
   return MPK_OK;
 }
 mpk_status check_batch(const mpk_token_batch* t) {
@@ -58,6 +58,10 @@ mpk_status fill_paged(const mpk_attn_shape* s, const mpk_token_batch* t,
       off(kv->k_pool, 16) || off(kv->v_pool, 16) || off(kv->page_table, 4) ||
       off(kv->seq_lens, 4) || off(d_status, 4))
     return MPK_ERR_INVALID_ARG;
+  // rows of the pool are 32-bit numbers (2^32 of them are more than the
+  // memory: 64 bytes each at least)
+  const double rows = (double)kv->num_pages * s->n_kv_heads * s->page_size;
+  if (rows > 4294967295.0) return MPK_ERR_UNSUPPORTED;
   const int64_t stride = (int64_t)kv->num_pages * s->n_kv_heads *
                          s->page_size * s->head_dim;
   p->k = static_cast<uint16_t*>(kv->k_pool) + layer * stride;

@@ -698,7 +698,10 @@ class PagedBatch(_OnDevice):
                 self._vec(prefix_len, n, torch.int32, w, "prefix_len"))
             if n < 1 or n > batch:
                 _refuse(w, "1 to batch groups")
-        self._keep = (q_start, group_start, prefix_len, status)
+        # (the pointers of these very tensors are used, whatever kv's
+        # attributes are set to later)
+        self._keep = (q_start, group_start, prefix_len, status, k, v,
+                      kv.page_table, kv.seq_lens)
         self._st = st
         self._refs = (ctypes.byref(self._shape), ctypes.byref(self._tok),
                       ctypes.byref(self._kv),

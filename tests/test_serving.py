@@ -43,6 +43,8 @@ BAD_PARTS = [
     (dict(s_n_kv_heads=0), INVALID), (dict(s_page_size=0), INVALID),
     (dict(s_max_pages_per_seq=0), INVALID), (dict(s_head_dim=96), UNSUPPORTED),
     (dict(s_page_size=1 << 20, s_max_pages_per_seq=1 << 20), UNSUPPORTED),
+    (dict(s_page_size=1 << 20, s_max_pages_per_seq=1025), UNSUPPORTED),
+    (dict(s_page_size=1 << 20, k_num_pages=2048), UNSUPPORTED),
     (dict(t_batch=0), INVALID), (dict(t_n_tokens=-1), INVALID),
     (dict(t_tokens_per_seq=3), INVALID), (dict(t_tokens_per_seq=-1), INVALID),
     (dict(t_batch=(1 << 20) + 1, t_tokens_per_seq=0), UNSUPPORTED),
@@ -535,6 +537,15 @@ def test_attend_reports_a_sequence_shorter_than_its_prefix():
 
 
 @gpu
+@pytest.mark.parametrize("cut", [[1, 3], [0, 2], [2, 2]])
+def test_attend_reports_sequences_outside_the_groups(cut):
+    c = Case(18, n=[1, 2, 1], ctx=[70, 70, 70], groups=([0, 3], [64]))
+    c.plan._keep[1].copy_(ref.as_dev(cut, torch.int32))
+    c.attend()
+    assert c.status.item() == mpk.MPK_ERR_INVALID_ARG
+
+
+@gpu
 @pytest.mark.parametrize("starts", [[0, 9, 0, 9, 0], [5, 4, 3, 2, 1],
                                     [-3, 2, 99, 1 << 30, 7]])
 def test_attend_stays_inside_its_memory_with_bad_starts(starts):
@@ -566,6 +577,17 @@ def test_attend_on_another_stream_and_in_a_graph():
     torch.cuda.synchronize()
     c.ctx = [64, 93, 200]
     c.check(out, lse)
+
+
+@gpu
+def test_plan_keeps_the_tensors_it_was_given():
+    c = Case(19, n=[1, 2], ctx=[33, 20])
+    want, wl = c.attend()
+    c.kv.seq_lens = torch.full((2,), 10 ** 6, dtype=torch.int32,
+                               device="cuda")
+    c.kv.page_table = torch.full_like(c.kv.page_table, -1)
+    out, lse = c.attend()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
 
 
 @gpu
