@@ -513,8 +513,9 @@ mpk_status mpk_prefix_attention(const mpk_attn_shape* shape,
  * accepted argmax_v p_v / noise[b][v] of the last row; ties take the lowest
  * index.  Outputs overlap no inputs, but for seq_lens_out.  With uniform in
  * [0, 1) and noise ~ Exp(1), the emitted tokens are
- * distributed as samples of p.  T <= 0 is greedy: a draft is accepted when it
- * is the row's argmax, the next token is the argmax.  NaN logits count as
+ * distributed as samples of p.  T <= 0 (or NaN) is greedy: a draft is accepted
+ * when it is the row's argmax, the next token is the argmax; other T count as
+ * the nearest of [1e-30, 1e30].  NaN logits count as
  * -inf, several +inf share the row; a row of nothing but -inf accepts nothing
  * and gives token -1. */
 typedef struct {

@@ -255,8 +255,8 @@ static mpk_status check_verify(const mpk_token_batch* tok,
   if (st != MPK_OK) return st;
   const bool none = tok->n_tokens == 0;   // outputs alone are written
   if (!v || v->vocab < 1 || v->max_out < 1 || (!none && !v->tokens) ||
-      (!none && !v->logits) || (!none && !v->uniform) || !v->noise || !v->n_accepted || !v->out_tokens ||
-      v->logits_stride < v->vocab || v->noise_stride < v->vocab ||
+      (!none && !v->logits) || (!none && !v->uniform) || !v->noise ||
+      !v->n_accepted || !v->out_tokens || v->logits_stride < v->vocab || v->noise_stride < v->vocab ||
       (v->draft && v->draft_stride < v->vocab) || off(v->tokens, 4) ||
       off(v->logits, 4) || off(v->draft, 4) || off(v->temperature, 4) ||
       off(v->uniform, 4) || off(v->noise, 4) || off(v->n_accepted, 4) ||

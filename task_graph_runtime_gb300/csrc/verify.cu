@@ -72,6 +72,14 @@ __device__ __forceinline__ RowInfo rows_of(const VerifyArgs& a, int b) {
   return r;
 }
 
+// T of sequence b: 0 or less (or NaN) is greedy.  Others are kept where
+// log2(e) / T is neither 0 nor infinite, whose products with an infinite or
+// zero difference of logits would be NaN.
+__device__ __forceinline__ float temperature(const VerifyArgs& a, int b) {
+  const float T = a.temperature ? __ldg(a.temperature + b) : 1.f;
+  return T > 0.f ? fminf(fmaxf(T, 1e-30f), 1e30f) : T;
+}
+
 __global__ void __launch_bounds__(kNT, 5)
     verify_stats(const __grid_constant__ VerifyArgs a) {
   sv_grid_wait();
@@ -119,7 +127,7 @@ __global__ void __launch_bounds__(kNT, 5)
   fetch(v0 + tid, w);  // on the way while the sequence is looked up
   const int b = sv_seq_of_warp(a.q_start, a.tokens_per_seq, a.batch, row);
   if (b < 0) return;
-  const float T = a.temperature ? __ldg(a.temperature + b) : 1.f;
+  const float T = temperature(a, b);
   const bool greedy = !(T > 0.f);
   const RowInfo ri = rows_of(a, b);
   const bool judges = row < ri.first + ri.n - 1;   // a draft comes after it
@@ -363,7 +371,9 @@ __device__ __forceinline__ unsigned long long race_slice(const Race& r,
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1)
       low = fmaxf(low, __shfl_xor_sync(0xffffffffu, low, s));
-    if (low > floor_) {
+    // (an infinite one comes from noise below the smallest normal number,
+    // which the fast reciprocal takes for 0: no bound)
+    if (low > floor_ && low < INFINITY) {
       // the other warps have less to work out next turn
       floor_ = low;
       if ((tid & 31) == 0) atomicMax(s_floor, __float_as_int(low));
@@ -395,7 +405,7 @@ __global__ void __launch_bounds__(kNT)
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   // (verify_stats has waited for what comes before it)
   RowInfo r = rows_of(a, b);
-  const float T = a.temperature ? __ldg(a.temperature + b) : 1.f;
+  const float T = temperature(a, b);
   if (r.n > a.max_out) {
     if (tid == 0) sv_latch(a.status, MPK_ERR_INVALID_ARG);
     r.n = a.max_out;

@@ -918,6 +918,34 @@ def test_verify_masked_logits(kind, temp):
 
 
 @gpu
+@pytest.mark.parametrize("kind", ["none", "probs", "logits"])
+def test_verify_extreme_temperatures(kind):
+    c = _verify_case(39, [3] * 5, 1003, kind, 1.0, near=0.2)
+    c["logits"][:, 500:] = -np.inf
+    c["temp"][:] = [np.inf, 3e38, 1e-39, 1e-45, np.nan]
+    o = _verify_run(c)
+    c["temp"][:] = [1e30, 1e30, 1e-30, 1e-30, 0]
+    _verify_check(c, o)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["none", "probs", "logits"])
+def test_verify_noise_below_the_normal_numbers(kind):
+    c = _verify_case(40, [1, 2, 1], 5003, kind, 1.0, near=0.2)
+    c["uniform"][:] = 1                         # (nearly) nothing accepted
+    c["noise"][:, 17] = 1e-39                   # e^-60 / 1e-39 is less
+    c["noise"][:, 900] = 1e-30                  # than e^-9 / 1e-30
+    c["logits"][:, 17] = -60
+    c["logits"][:, 900] = 0
+    if c["draft"] is not None:
+        c["draft"][:, [17, 900]] = 0 if kind == "probs" else -99
+    c["tokens"][:] = 5
+    o = _verify_run(c)
+    _verify_check(c, o)
+    assert o["nxt"].tolist() == [900] * 3
+
+
+@gpu
 def test_verify_ties_take_the_lowest_index():
     c = _verify_case(34, [1, 1], 4099, "none", np.array([0.0, 1.0]))
     c["logits"][:] = 0.5
