@@ -1,20 +1,25 @@
-"""Compile ``libmpk.so`` in-tree for sm_103a (nvcc + g++, no cmake).
+"""Compile ``libmpk.so`` in-tree for sm_103a (nvcc + g++, no cmake), and
+``_binding.so``, the serving calls' Python entry points, against this Python
+and torch.
 
-The translation units compile in parallel; the shared library lands
+The translation units compile in parallel; the shared libraries land
 next to this file.  ``python -m task_graph_runtime_gb300.build`` runs it."""
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libmpk.so")
+BINDING = os.path.join(PKG, "_binding.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 # the serving operators' kernels
 SERVE = ["append", "attend", "attend_d32", "attend_d64", "attend_d128",
@@ -43,6 +48,7 @@ def _run(cmd):
 def build(verbose: bool = False) -> str:
     cuda = _cuda_home()
     nvcc = os.path.join(cuda, "bin", "nvcc")
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
     os.makedirs(BUILD_DIR, exist_ok=True)
     inc = ["-I" + INCLUDE, "-I" + CSRC, "-I" + os.path.join(cuda, "include")]
     jobs = [
@@ -73,6 +79,12 @@ def build(verbose: bool = False) -> str:
         ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-pthread", "-c",
          os.path.join(CSRC, "protocol_sim.cpp"), "-o",
          os.path.join(BUILD_DIR, "protocol_sim.o")] + inc,
+        # (torch's and Python's headers count as system headers)
+        ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-c",
+         os.path.join(CSRC, "binding.cpp"), "-o",
+         os.path.join(BUILD_DIR, "binding.o"), "-isystem", torch + "/include",
+         "-isystem", torch + "/include/torch/csrc/api/include",
+         "-isystem", sysconfig.get_paths()["include"]] + inc,
     ]
     with concurrent.futures.ThreadPoolExecutor(len(jobs)) as ex:
         for out in ex.map(_run, jobs):
@@ -91,6 +103,13 @@ def build(verbose: bool = False) -> str:
                           "-Xcompiler", "-pthread",
                           "-Xlinker", "-rpath=" + os.path.join(cuda, "lib64")])
     os.replace(tmp, OUT)
+    # torch's libraries are in the process before this one is loaded
+    tmp = BINDING + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, os.path.join(BUILD_DIR, "binding.o"),
+          "-L" + PKG, "-l:libmpk.so", "-L" + os.path.join(torch, "lib"),
+          "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+          "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, BINDING)
     return OUT
 
 

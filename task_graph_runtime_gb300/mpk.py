@@ -563,6 +563,27 @@ def _refuse(where: str, what: str):
     raise MpkError(MPK_ERR_INVALID_ARG, f"{where}: {what}")
 
 
+def _failed(st, where: str, call: str):
+    """The answer of a call through _binding: a refusal's text, or a status."""
+    if isinstance(st, str):
+        _refuse(where, st)
+    raise MpkError(st, call)
+
+
+def _native():
+    """The module that checks the serving calls' tensors (csrc/binding.cpp)."""
+    load_library()
+    import torch  # noqa: F401  (its libraries have to be there first)
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise RuntimeError(
+            "the binding of the serving calls is missing or of another torch:"
+            " build it with `python -m task_graph_runtime_gb300.build` (no "
+            "fallback exists)") from e
+    return _binding
+
+
 class _OnDevice:
     """Calls go to the tensors' own device, whichever one is current."""
 
@@ -641,7 +662,7 @@ class Rope:
         self.device = dev
         self.c = _Rope(table.data_ptr(), int(table.shape[0]), rotary_dim,
                        int(bool(interleaved)))
-        self.ref = ctypes.byref(self.c)
+        self._address = ctypes.addressof(self.c)
 
 
 class PagedBatch(_OnDevice):
@@ -703,88 +724,45 @@ class PagedBatch(_OnDevice):
         self._keep = (q_start, group_start, prefix_len, status, k, v,
                       kv.page_table, kv.seq_lens)
         self._st = st
-        self._refs = (ctypes.byref(self._shape), ctypes.byref(self._tok),
-                      ctypes.byref(self._kv),
-                      ctypes.byref(self._groups) if self._groups else None)
+        native = _native()
+        at = ctypes.addressof
+        self._plan = native.paged(
+            at(self._shape), at(self._tok), at(self._kv),
+            at(self._groups) if self._groups else None, st, self.n_layers,
+            self._index)
+        self._append, self._attend = native.append, native.attend
         self._ws = None
-        lib = load_library()
-        self._c_append, self._c_attend = (lib.mpk_kv_append,
-                                          lib.mpk_prefix_attention)
-        self._c_attend_ws = lib.mpk_prefix_attention_workspace
-
-    def _rows(self, t, width, where, name):
-        """Pointer and row stride of [n_tokens, width] (or [n_tokens, heads,
-        head_dim]) bf16 rows whose values lie side by side."""
-        sh, st, n = t.shape, t.stride(), self.n_tokens
-        ok = t.dtype is self._bf16 and t.get_device() == self._index
-        if ok and len(sh) == 2:
-            ok = sh[1] == width and st[1] == 1 and sh[0] >= n
-        elif ok and len(sh) == 3:
-            ok = (sh[0] >= n and sh[2] == self.head_dim and
-                  sh[1] * sh[2] == width and st[2] == 1 and
-                  (sh[1] == 1 or st[1] == sh[2]))
-        else:
-            ok = False
-        if not ok:
-            _refuse(where, f"{name} must be bfloat16 [{n}, {width}] on "
-                           f"{self.device} with contiguous rows")
-        return t.data_ptr(), (st[0] if n > 1 else width)
 
     def append(self, layer: int, q, k, v, rope: Optional[Rope] = None,
                q_out=None, q_norm=None, k_norm=None, eps: float = 1e-6,
                stream=None):
         """mpk_kv_append: norm and rotate q and k, append k and v.  q may be
         None when q_out is."""
-        w = "PagedBatch.append"
-        if not 0 <= layer < self.n_layers:
-            _refuse(w, f"layer {layer} of {self.n_layers}")
-        kp, ks = self._rows(k, self.kv_width, w, "k")
-        vp, vs = self._rows(v, self.kv_width, w, "v")
-        qp = op = None
-        qs = os_ = 0
-        if q_out is not None:
-            if q is None:
-                _refuse(w, "q_out without q")
-            qp, qs = self._rows(q, self.q_width, w, "q")
-            op, os_ = self._rows(q_out, self.q_width, w, "q_out")
+        at = None
         if rope is not None:
             if rope.device != self.device:
-                _refuse(w, "rope is on another device")
-            rope = rope.ref
-        if q_norm is not None:
-            q_norm = self._vec(q_norm, self.head_dim, self._bf16, w, "q_norm")
-        if k_norm is not None:
-            k_norm = self._vec(k_norm, self.head_dim, self._bf16, w, "k_norm")
-        r = self._refs
-        st = self._call(self._c_append, r[0], r[1], r[2], layer, qp, qs, kp,
-                        ks, vp, vs, q_norm, k_norm, eps, rope, op, os_,
-                        self._st, self._stream(stream))
+                _refuse("PagedBatch.append", "rope is on another device")
+            at = rope._address
+        st = self._append(self._plan, layer, q, k, v, at, q_out, q_norm,
+                          k_norm, eps, stream)
         if st:
-            raise MpkError(st, "mpk_kv_append")
+            _failed(st, "PagedBatch.append", "mpk_kv_append")
 
     def attend(self, layer: int, q, out, lse=None, scale: float = 0.0,
                stream=None):
         """mpk_prefix_attention of the new tokens over the cache."""
-        w = "PagedBatch.attend"
-        if not 0 <= layer < self.n_layers:
-            _refuse(w, f"layer {layer} of {self.n_layers}")
-        qp, qs = self._rows(q, self.q_width, w, "q")
-        op, os_ = self._rows(out, self.q_width, w, "out")
-        lp = self._vec(lse, self.n_tokens * self.n_q_heads, self._f32, w,
-                       "lse")
-        r = self._refs
         if self._ws is None:
             import torch
-            n = self._c_attend_ws(r[0], r[1], self._groups.n_groups
-                                  if self._groups else 0)
+            n = load_library().mpk_prefix_attention_workspace(
+                ctypes.byref(self._shape), ctypes.byref(self._tok),
+                self._groups.n_groups if self._groups else 0)
             self._ws = torch.empty(max(n, 1), dtype=torch.uint8,
                                    device=self.device)
             self._ws_args = (self._ws.data_ptr(), self._ws.numel())
-        st = self._call(self._c_attend, r[0], r[1], r[3], r[2], layer, qp, qs,
-                        scale, op, os_, lp, *self._ws_args, self._st,
-                        self._stream(stream))
+        st = self._attend(self._plan, layer, q, out, lse, scale,
+                          *self._ws_args, stream)
         if st:
-            raise MpkError(st, "mpk_prefix_attention")
+            _failed(st, "PagedBatch.attend", "mpk_prefix_attention")
 
 
 class DraftVerifier(_OnDevice):
@@ -800,29 +778,20 @@ class DraftVerifier(_OnDevice):
         self._on(_cuda_device(probe, w))
         self.batch, self.n_tokens = batch, n_tokens
         self.vocab, self.max_out = vocab, max_out
-        lib = load_library()
-        self._c_verify = lib.mpk_verify_drafts
-        self._tok = TokenBatch(batch, n_tokens, None,
-                               n_tokens // max(batch, 1))
-        n = lib.mpk_verify_drafts_workspace(ctypes.byref(self._tok), vocab)
+        tok = TokenBatch(batch, n_tokens, None, n_tokens // max(batch, 1))
+        n = load_library().mpk_verify_drafts_workspace(ctypes.byref(tok),
+                                                       vocab)
         if n == 0 or not 1 <= max_out <= 128:
             raise MpkError(MPK_ERR_UNSUPPORTED if max_out > 128 else
                            MPK_ERR_INVALID_ARG, w)
         self._ws = torch.empty(n, dtype=torch.uint8, device=self.device)
         self._status = status
-        self._st = self._vec(status, 1, torch.int32, w, "status")
-        self._args = VerifyArgs(vocab=vocab, max_out=max_out)
-        self._refs = (ctypes.byref(self._tok), ctypes.byref(self._args))
-        self._ws_args = (self._ws.data_ptr(), n)
-
-    def _matrix(self, t, rows, where, name):
-        sh, st = t.shape, t.stride()
-        if (t.dtype is not self._f32 or t.get_device() != self._index or
-                len(sh) != 2 or sh[0] < rows or sh[1] != self.vocab or
-                (self.vocab > 1 and st[1] != 1)):
-            _refuse(where, f"{name} must be float32 [{rows}, {self.vocab}] on "
-                           f"{self.device} with contiguous rows")
-        return t.data_ptr(), (st[0] if rows > 1 else self.vocab)
+        native = _native()
+        self._judge = native.judge(
+            batch, n_tokens, vocab, max_out,
+            self._vec(status, 1, torch.int32, w, "status"),
+            self._ws.data_ptr(), n, self._index)
+        self._verify = native.verify
 
     def verify(self, tokens, logits, uniform, noise, n_accepted, out_tokens,
                q_start=None, draft=None, draft_is_logits: bool = False,
@@ -830,35 +799,9 @@ class DraftVerifier(_OnDevice):
                seq_lens=None, seq_lens_out=None, stream=None):
         """Accept or refuse the drafts and sample the next tokens; arguments
         and outputs as in include/mpk.h (mpk_verify_args)."""
-        w = "DraftVerifier.verify"
-        B, n, i32, f32, vec = (self.batch, self.n_tokens, self._i32,
-                               self._f32, self._vec)
-        if q_start is None:
-            if n % B:
-                _refuse(w, "n_tokens must be a multiple of the batch without "
-                           "q_start")
-            self._tok.q_start = None
-        else:
-            self._tok.q_start = vec(q_start, B + 1, i32, w, "q_start")
-        bo = B * self.max_out
-        a = self._args
-        a.tokens = vec(tokens, n, i32, w, "tokens")
-        a.logits, a.logits_stride = self._matrix(logits, n, w, "logits")
-        if draft is None:
-            a.draft = None
-        else:
-            a.draft, a.draft_stride = self._matrix(draft, n, w, "draft")
-            a.draft_is_logits = 1 if draft_is_logits else 0
-        a.temperature = vec(temperature, B, f32, w, "temperature")
-        a.uniform = vec(uniform, n, f32, w, "uniform")
-        a.noise, a.noise_stride = self._matrix(noise, B, w, "noise")
-        a.n_accepted = vec(n_accepted, B, i32, w, "n_accepted")
-        a.out_tokens = vec(out_tokens, bo, i32, w, "out_tokens")
-        a.logprobs = vec(logprobs, bo, f32, w, "logprobs")
-        a.next_tokens = vec(next_tokens, B, i32, w, "next_tokens")
-        a.seq_lens = vec(seq_lens, B, i32, w, "seq_lens")
-        a.seq_lens_out = vec(seq_lens_out, B, i32, w, "seq_lens_out")
-        st = self._call(self._c_verify, *self._refs, *self._ws_args,
-                        self._st, self._stream(stream))
+        st = self._verify(self._judge, tokens, logits, uniform, noise,
+                          n_accepted, out_tokens, q_start, draft,
+                          draft_is_logits, temperature, logprobs, next_tokens,
+                          seq_lens, seq_lens_out, stream)
         if st:
-            raise MpkError(st, "mpk_verify_drafts")
+            _failed(st, "DraftVerifier.verify", "mpk_verify_drafts")

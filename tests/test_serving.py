@@ -612,6 +612,83 @@ def test_attend_wrapper_refusals():
                                    c.kv.seq_lens), 4, 1)
 
 
+@gpu
+def test_wrapper_refusals_name_the_argument():
+    c = Case(20, n=[1, 1], ctx=[4, 9], d=64, hq=4, hkv=2)
+    W = c.hq * c.d
+    q, k = c.q.clone(), torch.zeros(2, 128, dtype=torch.bfloat16,
+                                    device="cuda")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    args = (0, q, k, k)
+
+    def refused(what, **kw):
+        with pytest.raises(mpk.MpkError, match=what):
+            c.plan.append(*[kw.pop(n, x) for n, x in zip(
+                ("layer", "q", "k", "v"), args)], **kw)
+    refused("layer 2", layer=2)
+    refused("layer -1", layer=-1)
+    for bad in (k.float(), k[:1], k[:, :120], k.cpu(), k.t(), [1.0], None,
+                k.view(2, 4, 32), k.repeat(1, 2)[:, ::2], k.to_sparse()):
+        refused("k must", k=bad)
+        refused("v must", v=bad)
+    refused("q must", q=q[:, 8:], q_out=q)
+    refused("q_out must", q_out=q.float())
+    refused("q_out without q", q=None, q_out=q)
+    for bad in (w[:63], w.float(), w.cpu(), w.repeat(2)[::2], 1):
+        refused("q_norm must", q_norm=bad)
+        refused("k_norm must", k_norm=bad)
+    with pytest.raises(TypeError):
+        c.plan.append(0, q, k, k, eps="much")
+    with pytest.raises(TypeError):
+        c.plan.append("0", q, k, k)
+    with pytest.raises(AttributeError):
+        c.plan.append(0, q, k, k, stream=1.5)
+    # heads apart, rows longer than they need be, a stream by name
+    c.k.zero_()
+    c.v.zero_()
+    x = torch.randn(3, 3 * W).bfloat16().cuda()
+    k3, v2 = x[:, :128].view(3, 2, 64), x[:, 200:328]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    c.plan.append(0, None, k3, v2, stream=s)
+    s.synchronize()
+    c.plan.append(1, None, k3, v2, stream=s.cuda_stream)
+    s.synchronize()
+    assert torch.equal(c.k[0], c.k[1]) and torch.equal(c.v[0], c.v[1])
+    assert c.k[0].any() and c.v[0].any()
+
+
+@gpu
+def test_verify_wrapper_refusals_name_the_argument():
+    f, i = torch.float32, torch.int32
+    z = lambda *s, t=f: torch.zeros(*s, dtype=t, device="cuda")
+    v = mpk.DraftVerifier(2, 5, 40, 3)
+    good = dict(tokens=z(5, t=i), logits=z(5, 40), uniform=z(5),
+                noise=z(2, 40) + 1, n_accepted=z(2, t=i),
+                out_tokens=z(2, 3, t=i), q_start=torch.tensor(
+                    [0, 3, 5], dtype=i, device="cuda"))
+    v.verify(**good)
+
+    def refused(what, **kw):
+        with pytest.raises(mpk.MpkError, match=what):
+            v.verify(**{**good, **kw})
+    refused("n_tokens must be a multiple", q_start=None)
+    for name, t in good.items():
+        refused(name, **{name: t.cpu()})
+        refused(name, **{name: t[:-1]})
+        refused(name, **{name: t.double()})
+    for name in ("logits", "noise", "draft"):
+        refused(name, **{name: z(5, 41)})
+        refused(name, **{name: z(5, 80)[:, ::2]})
+    for name in ("temperature", "logprobs"):
+        refused(name, **{name: z(1)})
+    for name in ("next_tokens", "seq_lens", "seq_lens_out"):
+        refused(name, **{name: z(2)})
+    for name in ("tokens", "uniform", "n_accepted", "out_tokens"):
+        refused("INVALID_ARG", **{name: None})      # the C call's own check
+    refused("logits must be a torch tensor", logits=None)
+
+
 # ------------------------------------------------------------------ append
 APPEND = {
     "one": dict(n=[1], ctx=[0]),
