@@ -38,14 +38,19 @@ __device__ __forceinline__ Found find(const AttendArgs& a, const AttnSet& s,
 // One warp joins the segments of one (token, query head): the prefix's and
 // the sequence's own.  Lane i fetches the maximum and sum of segment i, then
 // the partial outputs are added with their final weights, four loads in
-// flight.  A small grid goes through one turn of the same code on whatever
-// the workspace holds while it waits for the kernels before it, so that the
-// instructions and the pages' translations are at hand.  (Four heads a warp
-// took 6 us longer with 16 sequences, and as long with 256.)
-template <int D>
+// flight.
+// FEW: a grid of at most two CTAs an SM is all latency.  It goes through one
+// turn of the same code on whatever the workspace holds while it waits for the
+// kernels before it, so that the instructions and the pages' translations are
+// at hand, and has the first four segments on their way before it knows their
+// weights (16 sequences of 32 heads: the whole call 26.9 us, weights first 29.3).
+// More CTAs hide each other's latency and need the registers: 64 sequences
+// 49.7 us against 51.1.  (Eight or sixteen segments in flight: 0.4 and 1 us
+// longer with 16 sequences; four heads a warp: 6 us longer.)
+template <int D, bool FEW>
 __global__ void __launch_bounds__(kNT)
     attend_merge(const __grid_constant__ AttendArgs a) {
-  constexpr int V = D / 32;
+  constexpr int V = D / 32, G = 4;
   const PagedArgs& p = a.p;
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * (kNT / 32) + (threadIdx.x >> 5);
@@ -60,7 +65,7 @@ __global__ void __launch_bounds__(kNT)
   Ent pre{0, 0, 0, 0, 0};
   if (a.n_groups > 0) pre = att_group_ent(a, g);
   float m, l, acc[V];
-  for (int pass = gridDim.x <= 152 * 2 ? 0 : 1; pass < 2; ++pass) {
+  for (int pass = FEW ? 0 : 1; pass < 2; ++pass) {
     Found fp{0, 0}, fo{0, 1};            // (every set has a slot)
     if (pass == 1) {
       sv_grid_wait();
@@ -86,6 +91,31 @@ __global__ void __launch_bounds__(kNT)
         ml = q ? a.pre.ml[at] : a.own.ml[at];
         src = (q ? a.pre.part : a.own.part) + at * D;
       }
+      const int k = min(32, n - i0);
+      // segments q0 .. q0 + G - 1 on their way (a whole warp's row each)
+      float v[G][V];
+      auto row = [&](int q, float (&x)[V]) {
+        const float* s = reinterpret_cast<const float*>(__shfl_sync(
+            0xffffffffu, reinterpret_cast<unsigned long long>(src), q));
+        if constexpr (V == 4) {
+          const float4 u = *reinterpret_cast<const float4*>(s + lane * 4);
+          x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+        } else if constexpr (V == 2) {
+          const float2 u = *reinterpret_cast<const float2*>(s + lane * 2);
+          x[0] = u.x; x[1] = u.y;
+        } else {
+          x[0] = s[lane];
+        }
+      };
+      auto fetch = [&](int q0) {
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+#pragma unroll
+          for (int c = 0; c < V; ++c) v[j][c] = 0.f;
+          if (q0 + j < k) row(q0 + j, v[j]);   // (the same for all lanes)
+        }
+      };
+      if (FEW) fetch(0);
       float top = ml.x;
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1)
@@ -101,25 +131,27 @@ __global__ void __launch_bounds__(kNT)
       l = l * f + sum;
 #pragma unroll
       for (int q = 0; q < V; ++q) acc[q] *= f;
-      const int k = min(32, n - i0);
-#pragma unroll 4
-      for (int q = 0; q < k; ++q) {
-        const float* s = reinterpret_cast<const float*>(__shfl_sync(
-            0xffffffffu, reinterpret_cast<unsigned long long>(src), q));
-        const float x = __shfl_sync(0xffffffffu, wt, q);
-        float v[V];
-        if constexpr (V == 4) {
-          const float4 u = *reinterpret_cast<const float4*>(s + lane * 4);
-          v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-        } else if constexpr (V == 2) {
-          const float2 u = *reinterpret_cast<const float2*>(s + lane * 2);
-          v[0] = u.x; v[1] = u.y;
-        } else {
-          v[0] = s[lane];
-        }
-        // a segment in which the row saw nothing has weight 0 and zeros
+      // (a segment in which the row saw nothing has weight 0 and zeros)
+      auto add = [&](int q, const float (&x)[V]) {
+        const float w = __shfl_sync(0xffffffffu, wt, q);
 #pragma unroll
-        for (int c = 0; c < V; ++c) acc[c] = fmaf(v[c], x, acc[c]);
+        for (int c = 0; c < V; ++c) acc[c] = fmaf(x[c], w, acc[c]);
+      };
+      if constexpr (FEW) {
+        for (int q0 = 0;;) {
+#pragma unroll
+          for (int j = 0; j < G; ++j) add(q0 + j, v[j]);
+          q0 += G;
+          if (q0 >= k) break;
+          fetch(q0);
+        }
+      } else {
+#pragma unroll 4
+        for (int q = 0; q < k; ++q) {
+          float x[V];
+          row(q, x);
+          add(q, x);
+        }
       }
     }
   }
@@ -181,7 +213,9 @@ template <int D>
 cudaError_t run_merge(const AttendArgs& a, cudaStream_t s) {
   const int64_t warps = (int64_t)a.p.n_tokens * a.p.Hq;
   const int64_t blocks = (warps + kNT / 32 - 1) / (kNT / 32);
-  return sv_launch(attend_merge<D>, dim3((unsigned)blocks), kNT, 0, s, a);
+  return sv_launch(blocks <= 152 * 2 ? attend_merge<D, true>
+                                     : attend_merge<D, false>,
+                   dim3((unsigned)blocks), kNT, 0, s, a);
 }
 
 }  // namespace
