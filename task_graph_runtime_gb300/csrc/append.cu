@@ -11,7 +11,9 @@
 // heads are on the way while two are worked on.  Arithmetic is on pairs of
 // fp32 values (twice the rate), each operation rounded as by itself.
 //
-// Bound by HBM: every input and output byte moves once.
+// Bound by HBM: every input and output byte moves once.  Measured (32 / 8
+// heads of 128): 23 prompts of 1..4001 tokens, 921 MB, 158 us =
+// 5.8 TB/s; 8192 tokens, 205 MB, 42 us; one token of 16 sequences 3.6 us.
 #include "serve_dev.cuh"
 
 namespace mpk {

@@ -43,7 +43,8 @@ __device__ __forceinline__ Found find(const AttendArgs& a, const AttnSet& s,
 // turn of the same code on whatever the workspace holds while it waits for the
 // kernels before it, so that the instructions and the pages' translations are
 // at hand, and has the first four segments on their way before it knows their
-// weights (16 sequences of 32 heads: the whole call 26.9 us, weights first 29.3).
+// weights (16 sequences of 32 heads: the whole call 26.9 us, weights first
+// 29.3).
 // More CTAs hide each other's latency and need the registers: 64 sequences
 // 49.7 us against 51.1.  (Eight or sixteen segments in flight: 0.4 and 1 us
 // longer with 16 sequences; four heads a warp: 6 us longer.)

@@ -25,7 +25,7 @@
 // Pages that are a multiple of 8 tokens come as TMA boxes (blocks begin at
 // multiples of 64 keys, so that boxes do not cross pages), others key by key
 // in 16-byte copies; the computing warps clear the values of keys outside the
-// entity's.  They touch no list, table or length, and a stretch of many short
+// entity's.  These touch no list, table or length, and a stretch of many short
 // sequences streams like one long one: the chain lengths -> pages -> keys that
 // starts a sequence runs while earlier blocks are computed.
 //

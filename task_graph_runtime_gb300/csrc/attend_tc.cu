@@ -19,6 +19,13 @@
 // has grown by more than 2^kSlack over the one its weights are taken to
 // (their ratio cancels in O / l; 2^8 is far from any limit of fp32 or bf16), so
 // nearly every block leaves it alone.
+//
+// Measured: 256 rows x 32 heads over a prefix of 16384 (8 KV heads of 128),
+// 70 GFLOP, 68 us = 1.03 PFLOP/s.  A block of 256 x 128 takes 3520 cycles
+// against 2050 of its products: softmax (1590), product and next scores of a
+// slot follow one another, since weights and scores share their columns and
+// the 512 are full.  (Blocks of 64 keys with two score buffers a slot: 93 us,
+// the narrower products cost more than the wait.)
 #include "attend_plan.cuh"
 
 namespace mpk {
