@@ -158,6 +158,36 @@ def test_verify_refuses_bad_arguments(mpk_lib):
     assert mpk_lib.mpk_verify_drafts_workspace(ctypes.byref(big), 100) == 0
 
 
+def test_binding_refuses_before_it_calls():
+    """What the GPU wrappers' tests refuse, with tensors of the CPU."""
+    nat = mpk._native()
+    shape, tok = mpk.AttnShape(4, 2, 64, 16, 4), mpk.TokenBatch(2, 2, None, 1)
+    kv = mpk._KVCache()
+    at = ctypes.addressof
+    p = nat.paged(at(shape), at(tok), at(kv), None, None, 3, 0)
+    x = torch.zeros(2, 128, dtype=torch.bfloat16)
+    rest = (None, None, None, None, 1e-6, 0)
+    assert "k must be bfloat16 [2, 128] on cuda:0" in nat.append(
+        p, 0, None, x, x, *rest)
+    assert "k must be a torch tensor" == nat.append(p, 0, None, [1], x, *rest)
+    assert nat.append(p, 3, None, x, x, *rest) == "layer 3 of 3"
+    assert "q must be bfloat16 [2, 256]" in nat.attend(
+        p, 0, x, x, None, 0.0, 0, 0, 0)
+    j = nat.judge(2, 3, 10, 4, None, 0, 0, 0)
+    f = torch.zeros(3, 10)
+    assert "multiple of the batch" in nat.verify(
+        j, f, f, f, f, f, f, None, None, False, *[None] * 5, 0)
+    assert "q_start must be a contiguous Int tensor of 3" in nat.verify(
+        j, f, f, f, f, f, f, f, None, False, *[None] * 5, 0)
+    for call in (nat.append, nat.attend, nat.verify, nat.paged, nat.judge):
+        with pytest.raises(TypeError, match="arguments"):
+            call(p)
+    with pytest.raises(ValueError):              # another call's plan
+        nat.verify(p, f, f, f, f, f, f, None, None, False, *[None] * 5, 0)
+    with pytest.raises(TypeError):
+        nat.append(p, "0", None, x, x, *rest)
+
+
 def test_wrappers_refuse_tensors_of_the_cpu():
     k = torch.zeros(1, 2, 2, 16, 64, dtype=torch.bfloat16)
     kv = mpk.KVCache(k, k, torch.zeros(1, 2, dtype=torch.int32),
