@@ -451,6 +451,33 @@ def test_attend_stale_slots_do_not_reach_a_row(stale, groups):
 
 
 @gpu
+@pytest.mark.parametrize("page", [15, 16, 17, 20, 30, 47, 63, 94])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_attend_pages_that_end_inside_eight_keys(page, d):
+    # keys come eight at a time but where a page ends between them; contexts
+    # at and around the pages' ends, a prefix that ends there too
+    ctx = [3 * page + i for i in (-2, -1, 0, 1, 7, 8)]
+    c = Case(21, n=[1, 2, 1, 3, 1, 9], ctx=ctx, page=page, d=d, hq=8, hkv=2,
+             groups=([0, 3, 6], [3 * page - 2, 2 * page + 5]), stale=math.nan)
+    out, lse = c.attend()
+    assert c.status.item() == 0
+    c.check(out, lse)
+    assert torch.isfinite(out[:c.T].float()).all()
+
+
+@gpu
+@pytest.mark.parametrize("bad", [-1, 1 << 20])
+@pytest.mark.parametrize("col", [0, 1, 2])
+def test_attend_reports_a_bad_page_inside_eight_keys(bad, col):
+    c = Case(22, n=[1, 1], ctx=[50, 50], page=21)
+    c.kv.page_table[1, col] = bad
+    out, lse = c.attend()
+    assert c.status.item() == mpk.MPK_ERR_KV_PAGE
+    want, wl = Case(22, n=[1, 1], ctx=[50, 50], page=21).attend()
+    assert torch.equal(out[0], want[0]) and torch.equal(lse[0], wl[0])
+
+
+@gpu
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("n", [4, 40])
 def test_attend_values_of_later_tokens_do_not_reach_earlier_rows(bad, n):
